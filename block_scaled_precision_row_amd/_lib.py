@@ -29,6 +29,13 @@ _f32 = ctypes.c_float
 
 BSQ_MAX_GROUP = 8
 
+# include/bsq_serve.h
+BSQ_BF16, BSQ_FP16, BSQ_FP32 = 1, 2, 3
+BSQ_ROPE_HALF, BSQ_ROPE_INTERLEAVED = 1, 2
+BSQ_ROPE_PLAIN, BSQ_ROPE_LINEAR, BSQ_ROPE_NTK, BSQ_ROPE_YARN = 0, 1, 2, 3
+BSQ_ROPE_BACKWARD = 0x1
+BSQ_ATTN_FULL = 0x1
+
 
 class GemmProblem(ctypes.Structure):
     """bsq_gemm_problem: one linear of a grouped launch (device pointers as integers)."""
@@ -42,7 +49,14 @@ class WeightOnlyProblem(ctypes.Structure):
                 ("M", _i64), ("N", _i64), ("K", _i64)]
 
 
-# symbol -> (restype, argtypes); mirrors include/bsq.h
+class Kv8Cache(ctypes.Structure):
+    """bsq_kv8_cache: the paged E4M3 key/value cache of a call (device pointers as integers)."""
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("block_table", _p), ("seq_lens", _p),
+                ("num_pages", _i64), ("kv_heads", _i64), ("page_size", _i64), ("head_dim", _i64), ("batch", _i64),
+                ("max_pages", _i64), ("table_stride", _i64)]
+
+
+# symbol -> (restype, argtypes); mirrors include/bsq.h and include/bsq_serve.h
 SIGNATURES = {
     "bsq_abi_version": (_int, []),
     "bsq_status_string": (ctypes.c_char_p, [_int]),
@@ -77,6 +91,15 @@ SIGNATURES = {
                                    _p, _sz, _p]),
     "bsq_lora_down_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "bsq_lora_down": (_int, [_p, _i64, _p, _i64, _i64, _i64, _f32, _p, _p, _sz, _p]),
+    "bsq_rope_inv_freq": (_int, [_i64, ctypes.c_double, _int, ctypes.c_double, _i64, ctypes.c_double, ctypes.c_double,
+                                 _p, _p]),
+    "bsq_rope": (_int, [_int, _p, _i64, _i64, _p, _p, _i64, _int, _f32, _u32, _p, _i64, _i64, _i64, _i64, _i64, _p]),
+    "bsq_kv_append": (_int, [_int, ctypes.POINTER(Kv8Cache), _p, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _int,
+                             _f32, _p, _i64, _i64, _i64, _p, _i64, _i64, _p]),
+    "bsq_attention_kv8_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "bsq_attention_kv8": (_int, [_int, ctypes.POINTER(Kv8Cache), _p, _i64, _i64, _p, _i64, _i64, _i64, _f32, _i64,
+                                 _u32, _p, _i64, _i64, _p, _p, _sz, _p]),
+    "bsq_gemm_int4g": (_int, [_int, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _p]),
 }
 
 
@@ -559,3 +582,174 @@ def bsq_dequant_to_bf16(fmt, w, w_scale, w_scale2=None, out=None):
     _check("bsq_dequant_to_bf16", lib.bsq_dequant_to_bf16(fmt, _ptr(w), _ptr(w_scale), _ptr(w_scale2), N, K,
                                                           _ptr(out), _stream()))
     return out
+
+
+# ---- token serving (include/bsq_serve.h) ------------------------------------------
+# These run on the device of their tensors, on that device's current stream.
+
+_DTYPES = {torch.bfloat16: BSQ_BF16, torch.float16: BSQ_FP16, torch.float32: BSQ_FP32}
+
+
+def _call(fn, device, *args):
+    """lib.<fn>(*args, current stream) on `device`."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+        return
+    with torch.cuda.device(device):
+        _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _heads(x, dtypes, name):
+    """A [tokens, heads, dim] tensor, dim contiguous: (shape, token stride, head stride)."""
+    if x.dim() != 3 or x.dtype not in dtypes or not x.is_cuda:
+        raise ValueError("%s must be a 3-D tensor of %s on the GPU" % (name, " or ".join(map(str, dtypes))))
+    T, H, D = x.shape
+    st, sh, sd = x.stride()
+    if sd != 1 and D > 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return (T, H, D), (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
+def _like(x, shape, dtype, device, name):
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != device:
+        raise ValueError("%s must be a %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
+
+
+def _flat(x, shape, dtype, device, name):
+    _like(x, shape, dtype, device, name)
+    if not x.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return x.data_ptr()
+
+
+def bsq_rope_inv_freq(rot_dim, base, scaling=BSQ_ROPE_PLAIN, factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0):
+    """Inverse frequencies of a rotation over rot_dim elements, stretched for long contexts as `scaling` says:
+    (fp32 [rot_dim / 2] on the CPU, the factor of cosines and sines)."""
+    out = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float32)
+    factor_out = ctypes.c_float()
+    _check("bsq_rope_inv_freq", lib.bsq_rope_inv_freq(rot_dim, base, scaling, factor, trained_len, beta_fast, beta_slow,
+                                                      out.data_ptr(), ctypes.addressof(factor_out)))
+    return out, factor_out.value
+
+
+def bsq_rope(x, positions, inv_freq, layout=BSQ_ROPE_HALF, attn_factor=1.0, backward=False, y=None):
+    """x [T, H, D] (bf16, fp16 or fp32) with its first 2 * len(inv_freq) elements rotated to `positions`
+    (int64 [T]); backward: the gradient of x for x = the gradient of y. y may be x (in place)."""
+    (T, H, D), xt, xh = _heads(x, _DTYPES, "x")
+    dev = x.device
+    if y is None:
+        y = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+    _like(y, (T, H, D), x.dtype, dev, "y")
+    _, yt, yh = _heads(y, _DTYPES, "y")
+    pos = _flat(positions, (T,), torch.int64, dev, "positions")
+    pairs = inv_freq.shape[0]
+    freq = _flat(inv_freq, (pairs,), torch.float32, dev, "inv_freq")
+    _call("bsq_rope", dev, _DTYPES[x.dtype], x.data_ptr(), xt, xh, pos, freq, 2 * pairs, layout, attn_factor,
+          BSQ_ROPE_BACKWARD if backward else 0, y.data_ptr(), yt, yh, T, H, D)
+    return y
+
+
+def _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, dev):
+    """The descriptor of a cache and its call: (Kv8Cache, kv heads, head dim)."""
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache and v_cache must be 4-D, block_table 2-D")
+    P, H, page, D = k_cache.shape
+    B, W = block_table.shape
+    if block_table.dtype != torch.int32 or block_table.device != dev or (W > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be an int32 tensor on %s with unit stride along its rows" % dev)
+    c = Kv8Cache(_flat(k_cache, (P, H, page, D), torch.uint8, dev, "k_cache"),
+                 _flat(v_cache, (P, H, D, page), torch.uint8, dev, "v_cache"),
+                 _flat(k_scale, (P, H), torch.float32, dev, "k_scale"),
+                 _flat(v_scale, (P, H), torch.float32, dev, "v_scale"), block_table.data_ptr(),
+                 _flat(seq_lens, (B,), torch.int32, dev, "seq_lens"), P, H, page, D, B, W,
+                 block_table.stride(0) if B > 1 else W)
+    return c, H, D, _flat(cu_seqlens, (B + 1,), torch.int32, dev, "cu_seqlens")
+
+
+_HALF_TYPES = (torch.bfloat16, torch.float16)
+
+
+def bsq_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, inv_freq=None,
+                  layout=BSQ_ROPE_HALF, attn_factor=1.0, q=None, q_out=None):
+    """Append new tokens (k, v [T, kv_heads, dim], packed by cu_seqlens int32 [B + 1], the last ones of each
+    sequence's seq_lens int32 [B]) to the paged E4M3 cache: k_cache uint8 [pages, kv_heads, page, dim], v_cache uint8
+    [pages, kv_heads, dim, page], k_scale / v_scale fp32 [pages, kv_heads], block_table int32 [B, max_pages]. With
+    inv_freq the keys are rotated on the way, and q [T, q_heads, dim] into q_out (may be q), which is returned."""
+    dev = k.device
+    (T, H, D), kt, kh = _heads(k, _HALF_TYPES, "k")
+    _like(v, (T, H, D), k.dtype, dev, "v")
+    _, vt, vh = _heads(v, _HALF_TYPES, "v")
+    c, heads, dim, cu = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, dev)
+    if (heads, dim) != (H, D):
+        raise ValueError("k has %d heads of %d elements, the cache %d of %d" % (H, D, heads, dim))
+    freq, rot = None, 0
+    if inv_freq is not None:
+        freq, rot = _flat(inv_freq, (inv_freq.shape[0],), torch.float32, dev, "inv_freq"), 2 * inv_freq.shape[0]
+    qp = op = None
+    qt = qh = ot = oh = Hq = 0
+    if q is not None:
+        (_, Hq, _), qt, qh = _heads(q, _HALF_TYPES, "q")
+        _like(q, (T, Hq, D), k.dtype, dev, "q")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        _like(q_out, (T, Hq, D), q.dtype, dev, "q_out")
+        _, ot, oh = _heads(q_out, _HALF_TYPES, "q_out")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _call("bsq_kv_append", dev, _DTYPES[k.dtype], c, cu, T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, freq, rot,
+          layout, attn_factor, qp, qt, qh, Hq, op, ot, oh)
+    return q_out
+
+
+def bsq_attention_kv8_workspace_bytes(batch, T, max_q_len, q_heads, kv_heads, head_dim):
+    return lib.bsq_attention_kv8_workspace_bytes(batch, T, max_q_len, q_heads, kv_heads, head_dim)
+
+
+def bsq_attention_kv8(q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, max_q_len,
+                      softmax_scale=None, causal=True, window=0, y=None, lse=None, workspace=None):
+    """Attention of q [T, q_heads, dim] (packed by cu_seqlens, the last tokens of each sequence) over the paged E4M3
+    cache that bsq_kv_append fills; max_q_len: at least the most rows of a sequence (1 for a decode step).
+    softmax_scale: dim ** -0.5 where None. Returns (y [T, q_heads, dim], lse [T, q_heads] fp32)."""
+    dev = q.device
+    (T, Hq, D), qt, qh = _heads(q, _HALF_TYPES, "q")
+    c, H, dim, cu = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, dev)
+    if D != dim:
+        raise ValueError("q has heads of %d elements, the cache of %d" % (D, dim))
+    if y is None:
+        y = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    _like(y, (T, Hq, D), q.dtype, dev, "y")
+    _, yt, yh = _heads(y, _HALF_TYPES, "y")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    lse_p = _flat(lse, (T, Hq), torch.float32, dev, "lse")
+    if workspace is None:
+        n = lib.bsq_attention_kv8_workspace_bytes(c.batch, T, max_q_len, Hq, H, D)
+        if n:
+            workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on %s" % dev)
+    _call("bsq_attention_kv8", dev, _DTYPES[q.dtype], c, cu, T, max_q_len, q.data_ptr(), qt, qh, Hq,
+          D ** -0.5 if softmax_scale is None else softmax_scale, window, 0 if causal else BSQ_ATTN_FULL, y.data_ptr(),
+          yt, yh, lse_p, None if workspace is None else workspace.data_ptr(), _nbytes(workspace))
+    return y, lse
+
+
+def bsq_gemm_int4g(x, w, w_scale, w_zero=None, y=None):
+    """x [M, K] (bf16 or fp16), 4-bit codes w uint8 [N, K/2], w_scale [N, K/group] of x's type, zero points uint8
+    [N, K/group] (8 where None) -> y [M, N] of x's type."""
+    if x.dtype not in _HALF_TYPES:
+        raise ValueError("x must be bfloat16 or float16")
+    M, K, ldx = _rows(x, x.dtype, "x")
+    dev, N, groups = x.device, w.shape[0], w_scale.shape[1]
+    wp = _flat(w, (N, K // 2), torch.uint8, dev, "w")
+    sp = _flat(w_scale, (N, groups), x.dtype, dev, "w_scale")
+    zp = None if w_zero is None else _flat(w_zero, (N, groups), torch.uint8, dev, "w_zero")
+    if groups == 0 or K % groups:
+        raise ValueError("w_scale must have a column for each group of K")
+    if y is None:
+        y = torch.empty((M, N), dtype=x.dtype, device=dev)
+    _like(y, (M, N), x.dtype, dev, "y")
+    _, _, ldy = _rows(y, x.dtype, "y")
+    _call("bsq_gemm_int4g", dev, _DTYPES[x.dtype], x.data_ptr(), ldx, wp, sp, zp, K // groups, y.data_ptr(), ldy, M, N, K)
+    return y

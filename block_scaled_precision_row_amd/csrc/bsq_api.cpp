@@ -13,6 +13,7 @@
 #include <utility>
 
 #include "bsq_launch.hpp"
+#include "serve_launch.hpp"
 
 namespace {
 
@@ -148,6 +149,11 @@ bsq_status check_lora(int64_t ldx, const uint16_t* a, const uint16_t* b, int64_t
 }
 
 }  // namespace
+
+namespace bsq {
+bsq_status current_device_status() { return check_device(); }
+bsq_status hip_failure(hipError_t e) { return hip_fail(e); }
+}  // namespace bsq
 
 extern "C" {
 

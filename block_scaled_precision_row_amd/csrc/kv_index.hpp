@@ -1,0 +1,117 @@
+// Index arithmetic of the paged E4M3 key/value cache (include/bsq_serve.h), shared by the
+// kernels and, compiled for the host, by the audit that enumerates it on the CPU: everything that
+// turns device-side lengths and page tables into addresses is here, and clamps what it reads, so
+// that no table or length leads outside the tensors of a call.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace bsq {
+namespace kv {
+
+#define BSQ_HD __host__ __device__ __forceinline__
+
+struct Cache {
+  uint8_t* k;            // [pages][heads][page][dim]
+  uint8_t* v;            // [pages][heads][dim][page]
+  float* ks;             // [pages][heads]
+  float* vs;
+  const int32_t* table;  // [batch][table_stride]
+  const int32_t* lens;   // [batch]
+  int64_t table_stride;
+  int num_pages, heads, shift;  // page size 1 << shift
+  int dim, batch, max_pages;
+};
+
+constexpr int kTile = 64;  // tokens that a wave of the attention kernels takes at once
+
+// rows of sequence b in the packed tensors
+struct Rows {
+  int first, n;
+};
+BSQ_HD Rows rows_of(const int32_t* cu, int b, int64_t T) {
+  const int t = (int)T;
+  int lo = cu[b], hi = cu[b + 1];
+  lo = lo < 0 ? 0 : (lo > t ? t : lo);
+  hi = hi < lo ? lo : (hi > t ? t : hi);
+  return Rows{lo, hi - lo};
+}
+
+// tokens of sequence b that the table has room for
+BSQ_HD int tokens_of(const Cache& c, int b) {
+  const int len = c.lens[b], room = c.max_pages << c.shift;
+  return len < 0 ? 0 : (len > room ? room : len);
+}
+
+// the page of sequence b's token t, -1 where it is absent
+BSQ_HD int page_of(const Cache& c, int b, int t) {
+  const int j = t >> c.shift;
+  if (t < 0 || j >= c.max_pages) return -1;
+  const int id = c.table[(int64_t)b * c.table_stride + j];
+  return id < 0 || id >= c.num_pages ? -1 : id;
+}
+
+// offset of a page's codes of one head, in K and in V alike
+BSQ_HD int64_t codes_at(const Cache& c, int page, int head) {
+  return (((int64_t)page * c.heads + head) << c.shift) * c.dim;
+}
+
+// ---- append: one workgroup per touched page --------------------------------------------
+// Sequence b's n new tokens touch at most n / page + 2 pages, so giving it the slots from
+// first_slot(b) = cu[b] / page + 2 b on leaves room for them: first_slot(b + 1) - first_slot(b)
+// >= n / page + 2. A slot's sequence is the last b whose first slot is not behind it.
+BSQ_HD int64_t first_slot(const int32_t* cu, int b, int64_t T, int shift) {
+  const int t = cu[b];
+  return (int64_t)((t < 0 ? 0 : (t > (int)T ? (int)T : t)) >> shift) + 2 * (int64_t)b;
+}
+BSQ_HD int64_t append_slots(int64_t T, int64_t batch, int shift) { return (T >> shift) + 2 * batch; }
+
+// what slot `first_slot(b) + j` appends: tokens [at, at + n) of page `page`, from row `row` on
+struct Touched {
+  int page, at, n, row;
+};
+BSQ_HD Touched touched_page(const Cache& c, const int32_t* cu, int b, int64_t j, int64_t T) {
+  const Touched none{-1, 0, 0, 0};
+  const Rows r = rows_of(cu, b, T);
+  const int64_t len = c.lens[b], past = len - r.n;
+  if (r.n == 0 || past < 0) return none;
+  const int64_t start = ((past >> c.shift) + j) << c.shift;
+  if (start >= len || (start >> c.shift) >= c.max_pages) return none;
+  const int page = page_of(c, b, (int)start);
+  if (page < 0) return none;
+  const int64_t lo = past > start ? past : start;
+  const int64_t end = start + ((int64_t)1 << c.shift), hi = len < end ? len : end;
+  return Touched{page, (int)(lo - start), (int)(hi - lo), (int)(r.first + (lo - past))};
+}
+
+// ---- attention: the tokens of a sequence split over workgroups -----------------------------
+// Tokens that some row of rows [i0, i0 + rows) of a sequence's n sees: [lo, hi), lo a multiple
+// of kTile. `full`: no causal mask.
+struct Range {
+  int lo, hi;
+};
+BSQ_HD Range seen_range(int len, int room, int n, int i0, int rows, int64_t window, bool full) {
+  int64_t hi = full ? len : (int64_t)len - n + i0 + rows;
+  if (hi > len) hi = len;
+  if (hi > room) hi = room;
+  int64_t lo = 0;
+  if (window > 0) lo = (int64_t)len - n + i0 - window + 1;
+  if (lo < 0) lo = 0;
+  lo = lo / kTile * kTile;
+  return hi <= lo ? Range{0, 0} : Range{(int)lo, (int)hi};
+}
+BSQ_HD int tiles_of(Range r) { return (r.hi - r.lo + kTile - 1) / kTile; }
+
+// A sequence of `tiles` tiles is cut into pieces of at most `chunk`, one workgroup each (an
+// empty one keeps one piece, which writes its rows' zeros). With chunk = max(least,
+// ceil(total / target)) all sequences together have at most target + batch pieces.
+BSQ_HD int chunk_of(int64_t total, int target, int least) {
+  const int64_t c = (total + target - 1) / target;
+  return (int)(c < least ? least : (c > 0x7FFFFFFF ? 0x7FFFFFFF : c));
+}
+BSQ_HD int pieces_of(int tiles, int chunk) { return tiles == 0 ? 1 : (tiles - 1) / chunk + 1; }
+BSQ_HD int piece_begin(int tiles, int pieces, int i) { return (int)((int64_t)tiles * i / pieces); }
+
+}  // namespace kv
+}  // namespace bsq

@@ -1,0 +1,149 @@
+// Host-side audit of the paged cache's index arithmetic (built and run by tests/test_kv_audit.py;
+// no GPU involved): the functions of kv_index.hpp that the append and attention kernels take their
+// addresses from, over regular batches and over lengths and tables out of every range.
+//  * append: the slots give every touched page of every sequence exactly once, each new token is
+//    in exactly one, and rows, page ids and places lie inside their tensors whatever is read;
+//  * attention: the tokens that rows see are covered by the pieces exactly once, the pieces of a
+//    batch number at most target + batch, and every page looked up is a page of the pool or absent.
+// Prints one line and exits with 1 on the first violation.
+#include <cstdio>
+#include <cstdlib>
+#include <cstdint>
+#include <random>
+#include <set>
+#include <vector>
+
+#include "kv_index.hpp"
+
+using namespace bsq::kv;
+
+namespace {
+
+[[noreturn]] void fail(const char* what, long a, long b, long c, long d) {
+  std::printf("VIOLATION %s (%ld %ld %ld %ld)\n", what, a, b, c, d);
+  std::exit(1);
+}
+
+long g_checked = 0;
+
+int slot_sequence(const Cache& c, const int32_t* cu, int64_t T, int64_t slot) {
+  int b = -1;
+  for (int i = 0; i < c.batch; ++i)
+    if (first_slot(cu, i, T, c.shift) <= slot) b = i;
+  return b;
+}
+
+void check_append(const Cache& c, const std::vector<int32_t>& cu, int64_t T, bool regular) {
+  const int ps = 1 << c.shift;
+  const int64_t slots = append_slots(T, c.batch, c.shift);
+  std::vector<int> taken((size_t)T, 0);
+  std::set<std::pair<int, int64_t>> seen;
+  for (int64_t s = 0; s < slots; ++s) {
+    const int b = slot_sequence(c, cu.data(), T, s);
+    if (b < 0) continue;
+    const int64_t j = s - first_slot(cu.data(), b, T, c.shift);
+    const Touched t = touched_page(c, cu.data(), b, j, T);
+    if (t.page < 0) continue;
+    ++g_checked;
+    if (t.page >= c.num_pages) fail("page outside the pool", t.page, c.num_pages, b, s);
+    if (t.n < 1 || t.at < 0 || t.at + t.n > ps) fail("tokens outside the page", t.at, t.n, b, s);
+    if (t.row < 0 || t.row + t.n > T) fail("rows outside the tensor", t.row, t.n, b, s);
+    if (!seen.insert({b, j}).second) fail("a page twice", b, j, s, 0);
+    for (int i = 0; i < t.n; ++i) taken[(size_t)(t.row + i)]++;
+  }
+  if (!regular) return;
+  for (int b = 0; b < c.batch; ++b) {
+    const int n = cu[b + 1] - cu[b];
+    for (int i = 0; i < n; ++i) {
+      const int64_t pos = (int64_t)c.lens[b] - n + i;
+      const bool want = (int64_t)c.lens[b] >= n && page_of(c, b, (int)pos) >= 0;
+      if (taken[(size_t)(cu[b] + i)] != (want ? 1 : 0)) fail("a token not appended once", b, i, taken[(size_t)(cu[b] + i)], want);
+    }
+  }
+  for (int64_t t = cu[c.batch]; t < T; ++t)
+    if (taken[(size_t)t]) fail("a row of no sequence appended", t, 0, 0, 0);
+}
+
+void check_attention(const Cache& c, const std::vector<int32_t>& cu, int64_t T, int64_t window, bool full, int target,
+                     int least) {
+  const int room = c.max_pages << c.shift;
+  int64_t total = 0;
+  std::vector<int> tiles((size_t)c.batch, -1);
+  std::vector<Range> range((size_t)c.batch);
+  for (int b = 0; b < c.batch; ++b) {
+    const int n = rows_of(cu.data(), b, T).n;
+    if (n == 0) continue;
+    const int len = c.lens[b] < 0 ? 0 : c.lens[b];
+    range[b] = seen_range(len, room, n, 0, n, window, full);
+    tiles[b] = tiles_of(range[b]);
+    if (range[b].lo % kTile || range[b].lo < 0 || range[b].hi > room || tiles[b] < 0) fail("range", b, range[b].lo, range[b].hi, room);
+    for (int i = 0; i < n; ++i) {  // what a row sees lies inside
+      const int64_t pos = (int64_t)len - n + i;
+      int64_t hi = full ? len : pos + 1, lo = window > 0 ? pos - window + 1 : 0;
+      hi = hi > room ? room : hi;
+      lo = lo < 0 ? 0 : lo;
+      if (hi > lo && (lo < range[b].lo || hi > range[b].hi)) fail("a row sees past the range", b, i, lo, hi);
+    }
+    total += tiles[b];
+  }
+  const int chunk = target > 0 ? chunk_of(total, target, least) : 0x7FFFFFFF;
+  int64_t pieces = 0;
+  for (int b = 0; b < c.batch; ++b) {
+    if (tiles[b] < 0) continue;
+    const int p = pieces_of(tiles[b], chunk);
+    if (p < 1) fail("a sequence without a piece", b, p, tiles[b], chunk);
+    pieces += p;
+    if (piece_begin(tiles[b], p, 0) != 0 || piece_begin(tiles[b], p, p) != tiles[b]) fail("pieces do not cover", b, p, tiles[b], 0);
+    for (int i = 0; i < p; ++i) {
+      const int n = piece_begin(tiles[b], p, i + 1) - piece_begin(tiles[b], p, i);
+      if (n < 0 || n > chunk) fail("piece size", b, i, n, chunk);
+      ++g_checked;
+    }
+    for (int t = range[b].lo; t < range[b].hi && t < range[b].lo + 4096; t += 16) {
+      const int id = page_of(c, b, t);
+      if (id < -1 || id >= c.num_pages) fail("page outside the pool", b, t, id, 0);
+    }
+  }
+  if (pieces > (int64_t)target + c.batch) fail("more pieces than the grid holds", pieces, target, c.batch, 0);
+}
+
+}  // namespace
+
+int main() {
+  std::mt19937 rng(1);
+  auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+  for (int round = 0; round < 1500; ++round) {
+    Cache c{};
+    c.shift = pick(4, 8);
+    const int ps = 1 << c.shift;
+    c.heads = pick(1, 4);
+    c.dim = 64;
+    c.batch = pick(1, round % 10 == 0 ? 300 : 9);
+    c.max_pages = pick(1, 12);
+    c.table_stride = c.max_pages + pick(0, 3);
+    c.num_pages = pick(1, 40);
+    std::vector<int32_t> cu((size_t)c.batch + 1, 0), lens((size_t)c.batch), table((size_t)(c.batch * c.table_stride));
+    const bool regular = round % 4 != 3;
+    for (int b = 0; b < c.batch; ++b) {
+      const int n = pick(0, 3) == 0 ? 0 : (pick(0, 2) ? pick(1, 3) : pick(1, 3 * ps));
+      cu[b + 1] = cu[b] + n;
+      lens[b] = n + (pick(0, 2) ? pick(0, 6 * ps) : 0);
+      if (pick(0, 15) == 0) lens[b] = pick(0, n);          // fewer tokens than rows
+    }
+    for (auto& t : table) t = pick(0, 12) == 0 ? pick(-3, 60) : pick(0, c.num_pages - 1);
+    int64_t T = cu[c.batch] + (pick(0, 3) ? 0 : pick(0, 50));  // rows of no sequence behind
+    if (!regular) {
+      const int32_t wild[] = {-2147483647 - 1, -1, 0, 1, 1000, 2147483647};
+      for (auto& v : cu) if (pick(0, 2) == 0) v = wild[pick(0, 5)];
+      for (auto& v : lens) if (pick(0, 2) == 0) v = wild[pick(0, 5)];
+      for (auto& v : table) if (pick(0, 2) == 0) v = wild[pick(0, 5)];
+    }
+    c.table = table.data();
+    c.lens = lens.data();
+    if (T > 0) check_append(c, cu, T, regular);
+    for (int w = 0; w < 3; ++w)
+      check_attention(c, cu, T, w == 1 ? pick(1, 300) : 0, w == 2, pick(0, 3) ? pick(1, 600) : 0, pick(1, 8));
+  }
+  std::printf("ok: %ld pages and pieces checked\n", g_checked);
+  return 0;
+}
