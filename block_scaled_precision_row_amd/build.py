@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libbsq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quant.hip", "dequant.hip", "gemm_fp8.hip", "gemm_dec.hip", "gemm_w4a4.hip", "gemm_skinny.hip", "gemm_a16.hip", "lora.hip", "scratch.hip", "bsq_api.cpp",
-           "rope.hip", "kv_append.hip", "kv_attn.hip", "gemm_int4.hip", "bsq_serve.cpp"]
+           "rope.hip", "kv_append.hip", "kv_attn.hip", "kv_prompt.hip", "gemm_int4.hip", "bsq_serve.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",

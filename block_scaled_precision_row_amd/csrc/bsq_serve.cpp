@@ -182,6 +182,7 @@ bool attention_shape(int64_t batch, int64_t T, int64_t max_q_len, int64_t q_head
   if (batch < 0 || batch > 65536 || T < 0 || T > kMaxRows) return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
   if (kv_heads < 1 || kv_heads > 1024 || q_heads < 1 || q_heads % kv_heads != 0 || q_heads > 65535) return false;
+  if ((T * (q_heads / kv_heads) / 128 + batch) * kv_heads >= kMaxBlocks) return false;
   return max_q_len >= 0 && (max_q_len > 0 || T == 0);
 }
 }  // namespace

@@ -1,0 +1,205 @@
+// What the attention kernels over the paged E4M3 cache share: arguments, the rows' masks, the tile of 64
+// tokens in LDS and its loads, and the treatment of what a row must not see.
+#pragma once
+
+#include "bsq_launch.hpp"
+#include "serve_device.hpp"
+
+namespace bsq {
+namespace attn {
+
+using kv::Cache;
+
+struct Args {
+  Cache c;
+  const int32_t* cu;
+  int64_t T;
+  const uint16_t* q;
+  uint16_t* y;
+  float* lse;
+  int64_t qt, qh, yt, yh;
+  int q_heads, group;
+  float scale2;  // softmax_scale * log2(e)
+  int64_t window;
+  bool full;
+  bool flip;            // a negative softmax_scale: scale2 is its magnitude and q enters negated
+  int max_q_len;
+  int small;            // most rows (tokens times group) of a sequence that the step kernel takes
+  int target, least;    // step kernel: pieces of all sequences together, least tiles of a piece
+  int splits;           // prompt kernel: parts that a block's tokens are cut into
+  float* part_o;        // partial results: step [piece][kv head][16][D], prompt [block][kv head][split][128][D]
+  float* part_ml;       // their maxima (of scores times log2 e) and sums [...][2]
+};
+
+constexpr float kLn2 = 0.693147180559945309f;
+
+__device__ __forceinline__ int room_of(const Cache& c) { return c.max_pages << c.shift; }
+
+// row R (token R / group, query head R % group) of a sequence of n rows and what it sees
+struct Row {
+  int i;           // token of the sequence's n, -1 for none
+  int head;        // query head
+  int lo, hi;      // tokens seen
+};
+__device__ __forceinline__ Row row_at(const Args& a, int R, int kvh, int n, int len, int room) {
+  Row r;
+  r.i = R / a.group;
+  r.head = kvh * a.group + (R - r.i * a.group);
+  if (r.i >= n || r.i >= a.max_q_len) {
+    r.i = -1;
+    r.lo = 0;
+    r.hi = 0x7FFFFFFF;  // (computed, never stored: it must not ask for a mask)
+    return r;
+  }
+  const int64_t pos = (int64_t)len - n + r.i;
+  int64_t hi = a.full ? len : pos + 1;
+  hi = hi > len ? len : hi;
+  hi = hi > room ? room : hi;
+  r.hi = hi < 0 ? 0 : (int)hi;
+  const int64_t lo = a.window > 0 ? pos - a.window + 1 : 0;
+  r.lo = lo < 0 ? 0 : (lo > 0x7FFFFFFF ? 0x7FFFFFFF : (int)lo);
+  return r;
+}
+// bytes [lo, hi) of the 16 of a lane's granule stay, the others become 0
+__device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
+  lo = lo < 0 ? 0 : (lo > 4 ? 4 : lo);
+  hi = hi < 0 ? 0 : (hi > 4 ? 4 : hi);
+  const uint32_t up = hi == 4 ? 0xFFFFFFFFu : (1u << (8 * hi)) - 1u;
+  const uint32_t below = lo == 4 ? 0xFFFFFFFFu : (1u << (8 * lo)) - 1u;
+  return up & ~below;
+}
+// 0x80 in every byte of w that is a NaN code
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// the 64 tokens' bits of one element
+__device__ __forceinline__ unsigned long long nan_map(const uint16_t* p) {
+  return (unsigned long long)p[0] | (unsigned long long)p[1] << 16 | (unsigned long long)p[2] << 32 |
+         (unsigned long long)p[3] << 48;
+}
+
+template <class E>
+union Frag {  // an MFMA operand of eight 16-bit values
+  typename E::vec8 v;
+  typename E::vec2 p[4];
+  uint32_t u[4];
+  uint4 q;
+};
+// eight E4M3 codes times 2^exponent(scale)
+template <class E>
+__device__ __forceinline__ typename E::vec8 dec8(uint32_t lo, uint32_t hi, float scale) {
+  Frag<E> f;
+  f.p[0] = E::template dec<false>(lo, scale);
+  f.p[1] = E::template dec<true>(lo, scale);
+  f.p[2] = E::template dec<false>(hi, scale);
+  f.p[3] = E::template dec<true>(hi, scale);
+  return f.v;
+}
+
+
+// ---- a tile of 64 tokens in LDS (layout: kv_index.hpp) -------------------------------------
+constexpr int tile_bytes(int D) { return 128 * D; }  // K, then V
+constexpr int tile_loads(int D) { return D / 8; }    // of 1 KB
+
+// 16 bytes a lane from `p` to LDS at `lds` + 16 lane. Inline assembly, so that the compiler does not
+// make every LDS read wait for it; callers wait (wait_loads) before they read. (One wait state
+// between the write of M0 and its use.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+template <int n>
+__device__ __forceinline__ void wait_loads() {  // until at most n vector-memory operations are outstanding
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+
+// The pages of up to 16 tiles of a wave, lane l's granule l % 4 of tile l / 4: page (-1: absent) and scales.
+struct Pages {
+  int id;
+  float ks, vs;
+  // tile i starts at token t0 + stride * i; tokens from `end` on are not looked up
+  __device__ __forceinline__ void load(const Cache& c, int b, int head, int t0, int stride, int end) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)t0 + (int64_t)stride * (lane >> 2) + 16 * (lane & 3);
+    id = t < end ? kv::page_of(c, b, (int)t) : -1;
+    const int64_t at = (int64_t)(id < 0 ? 0 : id) * c.heads + head;
+    ks = c.ks[at];
+    vs = c.vs[at];
+  }
+  __device__ __forceinline__ int page(int tile, int gran) const { return __shfl(id, (tile & 15) * 4 + gran, 64); }
+  __device__ __forceinline__ float kscale(int tile, int gran) const { return __shfl(ks, (tile & 15) * 4 + gran, 64); }
+  __device__ __forceinline__ float vscale(int tile, int gran) const { return __shfl(vs, (tile & 15) * 4 + gran, 64); }
+};
+
+// Issues loads [first, last) of the tile at token t0 (its tile number `tile` in `pages`) into LDS at `lds`. An
+// absent page's place is filled from page 0, whose codes are hidden afterwards.
+template <int D, kv::Kind kind>
+struct TileLoads {
+  int k_lane[D / 64];  // granule 0's offsets; another granule exchanges pieces: an exclusive or
+  int v_gran, v_col;
+  __device__ __forceinline__ TileLoads(const Cache& c) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) k_lane[i] = kv::k_source<D, kind>(i, 0, lane);
+    const kv::VSource v = kv::v_source(lane, kv::v_run(1 << c.shift));
+    v_gran = v.gran;
+    v_col = v.col;
+  }
+  template <int first, int last>
+  __device__ __forceinline__ void issue(const Cache& c, const Pages& pages, int tile, int t0, int head,
+                                        uint32_t lds) const {
+    const int ps = 1 << c.shift;
+    const int vid = pages.page(tile, v_gran);
+    const uint8_t* vp = c.v + kv::codes_at(c, vid < 0 ? 0 : vid, head) + (int64_t)v_col * ps +
+                        ((t0 + 16 * v_gran) & (ps - 1));
+#pragma unroll
+    for (int n = first; n < last; ++n) {
+      if (n < D / 16) {
+        const int gran = n / (D / 64), i = n % (D / 64);
+        const int kid = __builtin_amdgcn_readlane(pages.id, (tile & 15) * 4 + gran);
+        const uint8_t* kp = c.k + kv::codes_at(c, kid < 0 ? 0 : kid, head) +
+                            (int64_t)((t0 + 16 * gran) & (ps - 1)) * D;
+        load_to_lds(kp + (k_lane[i] ^ (16 * kv::k_flip<D, kind>(16 * gran))), lds + 1024 * n);
+      } else {
+        load_to_lds(vp + (int64_t)16 * (n - D / 16) * ps, lds + 1024 * n);
+      }
+    }
+  }
+};
+
+// Hides tokens of a lane's 16 V codes: bytes outside [lo, hi) become 0. NaN codes among the others become 0
+// too and are returned as bits (a row that does not see such a token must not meet it as 0 * NaN).
+__device__ __forceinline__ uint32_t hide_codes(uint4& v, int lo, int hi) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] &= byte_mask(lo - 4 * i, hi - 4 * i);
+    const uint32_t nb = nan_bytes(w[i]);
+    bits |= ((nb >> 7 & 1u) | (nb >> 14 & 2u) | (nb >> 21 & 4u) | (nb >> 28 & 8u)) << (4 * i);
+    w[i] &= ~((nb >> 7) * 0xFFu);
+  }
+  return bits;
+}
+// the tokens of a tile at t0 that a row sees, as bits
+__device__ __forceinline__ unsigned long long seen_bits(const Row& row, int t0) {
+  const int lo = row.lo - t0, hi = row.hi - t0;
+  unsigned long long s = ~0ull;
+  if (lo > 0) s = lo >= 64 ? 0ull : s << lo;
+  if (hi < 64) s = hi <= 0 ? 0ull : s & ((1ull << hi) - 1ull);
+  return s;
+}
+
+template <class E>
+__device__ __forceinline__ uint4 negated(uint4 q, bool flip) {
+  const uint32_t m = flip ? 0x80008000u : 0u;
+  return make_uint4(q.x ^ m, q.y ^ m, q.z ^ m, q.w ^ m);
+}
+
+}  // namespace attn
+
+// the prompt kernel (kv_prompt.hip): sequences of more than `a.small` rows; blocks of 128 rows
+hipError_t launch_attn_prompt(bsq_dtype dt, const attn::Args& a, hipStream_t s);
+int64_t prompt_blocks(int64_t T, int64_t batch, int64_t group);
+
+}  // namespace bsq

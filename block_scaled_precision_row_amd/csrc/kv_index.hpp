@@ -113,5 +113,51 @@ BSQ_HD int chunk_of(int64_t total, int target, int least) {
 BSQ_HD int pieces_of(int tiles, int chunk) { return tiles == 0 ? 1 : (tiles - 1) / chunk + 1; }
 BSQ_HD int piece_begin(int tiles, int pieces, int i) { return (int)((int64_t)tiles * i / pieces); }
 
+// ---- a tile of 64 tokens of one head in LDS ---------------------------------------------
+// K [token][D], then V [D / 16][slot][16 tokens], loaded 1 KB an instruction, lane l's 16 bytes at 16 l.
+// What a lane fetches is permuted within a granule (16 tokens) so that neighbouring lanes read
+// neighbouring 16-byte pieces of memory, and the operand reads meet no bank conflict: the 16 lanes that a
+// 16-byte LDS read serves at once have to fall into different sixteenths of 256 bytes. Those lanes
+// are, for the step kernel, tokens 16 g + r (r < 4, g < 4) and, for the prompt kernel, tokens
+// 32 h + 4 a + b (h, a < 2, b < 4), at one piece; for V 16 elements at one granule.
+enum Kind : int { kStep = 0, kPrompt = 1 };
+template <int D, Kind kind>
+BSQ_HD int k_flip(int token) {  // pieces of a K row are exchanged by this
+  const int gran = token >> 4 & 3;
+  if (kind == kStep) {
+    if (D == 64) return gran;
+    return D == 128 ? (token >> 1 & 1) | gran << 1 : (token & 3) | gran << 2;
+  }
+  const int half = gran >> 1;
+  if (D == 64) return (token >> 2 & 1) | half << 1;
+  return D == 128 ? (token >> 1 & 3) | half << 2 : (token & 7) | half << 3;
+}
+// byte of a granule's K codes that lane `lane` fetches in its load `i` of D / 64, granule `gran`
+template <int D, Kind kind>
+BSQ_HD int k_source(int i, int gran, int lane) {
+  const int at = 1024 * i + 16 * lane, token = at / D, piece = at % D / 16;
+  return token * D + 16 * (piece ^ k_flip<D, kind>(16 * gran + token));
+}
+// where piece `piece` (16 elements) of a token lies in the tile
+template <int D, Kind kind>
+BSQ_HD int k_at(int token, int piece) {
+  return token * D + 16 * (piece ^ k_flip<D, kind>(token));
+}
+// V: granules of an element that lie side by side in a page (at most a tile's four)
+BSQ_HD int v_run(int page) { return page >= 64 ? 4 : page / 16; }
+// where the 16 tokens of granule g of element `d` lie in the tile's V
+BSQ_HD int v_at(int d, int g, int gp) {
+  const int c = d & 15;
+  return (d >> 4) * 1024 + 16 * ((g / gp) * (16 * gp) + c * gp + ((g % gp) ^ (c * gp >> 4)));
+}
+// granule and element (of 16) that lane `lane` fetches in each of its V loads
+struct VSource {
+  int gran, col;
+};
+BSQ_HD VSource v_source(int lane, int gp) {
+  const int run = lane / (16 * gp), rest = lane % (16 * gp), col = rest / gp;
+  return VSource{run * gp + ((rest % gp) ^ (col * gp >> 4)), col};
+}
+
 }  // namespace kv
 }  // namespace bsq

@@ -1,0 +1,339 @@
+// Attention of many rows over the paged E4M3 cache (prompts and their chunks, wide groups): blocks of 128 rows
+// (token, query head of the group) of one sequence and kv head, 32 to a wave, against tiles of 64
+// tokens that the four waves share in LDS.
+//
+// S^T = K Q^T on 32x32x16 MFMA, then O^T += V^T P^T on the same. A lane of the first product's result holds
+// column (query row) l % 32 and rows 8 a + 4 (l / 32) + b (a, b < 4); row 8 a + 4 h + b of K tile j is taken to
+// be token 32 h + 16 j + 4 a + b, so that a lane holds the 16 consecutive tokens of granule 2 (l / 32) + j in
+// tile j: one scale of K and of V each, and P in the order in which the second product wants its operand.
+//
+// Bound by the matrix cores and, as near, by the vector instructions of the softmax and the decoding of E4M3
+// (two values an instruction). Tiles come into two LDS buffers, one in flight while the other is
+// worked on, with one barrier a tile.
+#include "kv_attn.hpp"
+
+namespace bsq {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kBlock = 128;
+
+// Blocks of sequence b start at first_block(b) = cu[b] * group / 128 + b; n tokens need at most
+// n * group / 128 + 1 of them.
+__device__ __forceinline__ int64_t first_block(const Args& a, int b) {
+  const int t = a.cu[b], T = (int)a.T;
+  return (int64_t)(t < 0 ? 0 : (t > T ? T : t)) * a.group / kBlock + b;
+}
+// the last b whose first block is at most `id`, -1 if none: 64 candidates a step
+__device__ __forceinline__ int block_sequence(const Args& a, int64_t id) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.c.batch;
+  while (true) {
+    const int step = (n + 63) >> 6;
+    const bool in = lane * step < n && first_block(a, lo + lane * step) <= id;
+    const int cnt = __popcll(__ballot(in));
+    if (cnt == 0) return -1;
+    lo += (cnt - 1) * step;
+    n = step < n - (cnt - 1) * step ? step : n - (cnt - 1) * step;
+    if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+  }
+}
+
+__device__ __forceinline__ int min32(int v) {  // over the 32 columns
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    const int o = __shfl_xor(v, off, 64);
+    v = o < v ? o : v;
+  }
+  return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ int max32(int v) { return -min32(-v); }
+
+// a block's rows and the tokens they see
+struct Block {
+  int b, r0;  // sequence, first row of its n * group
+  kv::Rows rows;
+  int len;
+  kv::Range range;
+};
+__device__ __forceinline__ bool find_block(const Args& a, int64_t id, Block& o) {
+  o.b = block_sequence(a, id);
+  if (o.b < 0) return false;
+  o.rows = kv::rows_of(a.cu, o.b, a.T);
+  const int64_t all = (int64_t)o.rows.n * a.group, r0 = (id - first_block(a, o.b)) * kBlock;
+  if (all <= a.small || r0 >= all || r0 / a.group >= a.max_q_len) return false;
+  o.r0 = (int)r0;
+  const int len = a.c.lens[o.b];
+  o.len = len < 0 ? 0 : len;
+  const int i0 = o.r0 / a.group;
+  const int64_t i1 = (r0 + kBlock - 1) / a.group;
+  const int last = i1 < o.rows.n - 1 ? (int)i1 : o.rows.n - 1;
+  o.range = kv::seen_range(o.len, room_of(a.c), o.rows.n, i0, last - i0 + 1, a.window, a.full);
+  return true;
+}
+// parts that a block's tiles are cut into: none of less than eight
+__device__ __forceinline__ int parts_of(const Args& a, int tiles) {
+  const int most = tiles / 8 < 1 ? 1 : tiles / 8;
+  return a.splits < most ? a.splits : most;
+}
+
+constexpr int prompt_lds(int D) { return 2 * tile_bytes(D) + 4 * 32 * 8; }  // buffers; the waves' NaN maps
+
+template <class E, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt(Args a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  uint16_t* sh_nan = reinterpret_cast<uint16_t*>(smem + 2 * tile_bytes(D));  // [wave][32 elements][4 granules]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, h = lane >> 5;
+  // later blocks see more tokens: they go first; neighbouring workgroups, which go to different XCDs, take
+  // different heads, so that an XCD's L2 holds few of them
+  const int kvh = blockIdx.x % a.c.heads;
+  const int64_t id = (gridDim.x - 1 - blockIdx.x) / a.c.heads;
+  Block blk;
+  if (!find_block(a, id, blk)) return;
+  const int tiles = kv::tiles_of(blk.range), parts = parts_of(a, tiles);
+  if ((int)blockIdx.y >= parts) return;
+  const int tile0 = kv::piece_begin(tiles, parts, blockIdx.y), tile1 = kv::piece_begin(tiles, parts, blockIdx.y + 1);
+  const int count = tile1 - tile0, first = blk.range.lo + kv::kTile * tile0;
+  const int room = room_of(a.c);
+
+  const uint32_t lds = lds_offset(smem);
+  const TileLoads<D, kv::kPrompt> loads(a.c);
+  constexpr int kMine = tile_loads(D) / 4;  // a wave's share of a tile's loads
+  Pages pages;
+  auto issue = [&](int tile, int t0, uint32_t at) __attribute__((always_inline)) {
+    if (wave == 0) loads.template issue<0, kMine>(a.c, pages, tile, t0, kvh, at);
+    else if (wave == 1) loads.template issue<kMine, 2 * kMine>(a.c, pages, tile, t0, kvh, at);
+    else if (wave == 2) loads.template issue<2 * kMine, 3 * kMine>(a.c, pages, tile, t0, kvh, at);
+    else loads.template issue<3 * kMine, 4 * kMine>(a.c, pages, tile, t0, kvh, at);
+  };
+  if (count > 0) {
+    pages.load(a.c, blk.b, kvh, first, kv::kTile, blk.range.hi);
+    issue(0, first, lds);
+  }
+
+  const int R = blk.r0 + 32 * wave + col;
+  const Row row = row_at(a, R, kvh, blk.rows.n, blk.len, room);
+  const int any_lo = min32(row.i < 0 ? 0x7FFFFFFF : row.lo), any_hi = max32(row.i < 0 ? 0 : row.hi);
+  const int all_lo = max32(row.i < 0 ? 0 : row.lo), all_hi = min32(row.hi);
+  Frag<E> q[D / 16];  // elements 32 (s / 2) + 16 h + 8 (s % 2) + 0..7
+  {
+    const uint16_t* qr = a.q + (int64_t)(blk.rows.first + (row.i < 0 ? 0 : row.i)) * a.qt + (int64_t)row.head * a.qh;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      q[s].q = row.i < 0 ? make_uint4(0, 0, 0, 0)
+                         : negated<E>(*reinterpret_cast<const uint4*>(qr + 32 * (s >> 1) + 16 * h + 8 * (s & 1)), a.flip);
+  }
+  const int k_token = 32 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);  // K tile 0's row; tile 1's is 16 on
+  const int gp = kv::v_run(1 << a.c.shift);
+  int v_off[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) v_off[j] = kv::v_at(col, 2 * h + j, gp);
+
+  v16f acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+
+  for (int it = 0; it < count; ++it) {
+    const int t0 = first + kv::kTile * it;
+    int vid[2];
+    float ks[2], vs[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      vid[j] = pages.page(it, 2 * h + j);
+      ks[j] = pages.kscale(it, 2 * h + j) * a.scale2;
+      vs[j] = pages.vscale(it, 2 * h + j);
+    }
+    wait_loads<0>();
+    __syncthreads();
+    if (it + 1 < count) {
+      if (((it + 1) & 15) == 0) pages.load(a.c, blk.b, kvh, t0 + kv::kTile, kv::kTile, blk.range.hi);
+      issue(it + 1, t0 + kv::kTile, lds + ((it + 1) & 1) * tile_bytes(D));
+    }
+    if (t0 >= any_hi || t0 + kv::kTile <= any_lo) continue;  // nothing for this wave's rows
+    const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
+    const uint8_t* vb = kb + 64 * D;
+
+    v16f s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[j][r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 k = *reinterpret_cast<const uint4*>(kb + kv::k_at<D, kv::kPrompt>(k_token + 16 * j, 2 * i + h));
+        s[j] = E::mfma32(dec8<E>(k.x, k.y, 1.0f), q[2 * i].v, s[j]);
+        s[j] = E::mfma32(dec8<E>(k.z, k.w, 1.0f), q[2 * i + 1].v, s[j]);
+      }
+    }
+    const bool masked = t0 < all_lo || t0 + kv::kTile > all_hi || __ballot(vid[0] < 0 || vid[1] < 0) != 0;
+    float top = -INFINITY;
+    if (masked) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int vt = t0 + 32 * h + 16 * j, lo = vid[j] < 0 ? 16 : row.lo - vt, hi = row.hi - vt;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[j][r] = r >= lo && r < hi ? s[j][r] * ks[j] : -INFINITY;
+          top = fmaxf(top, s[j][r]);
+        }
+        ks[j] = 1.0f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float t = s[j][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) t = fmaxf(t, s[j][r]);
+        top = fmaxf(top, t * ks[j]);
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float mn = fmaxf(m, top);
+    const float base = mn == -INFINITY ? 0.0f : mn;
+    if (__ballot(mn != m)) {
+      const float alpha = __builtin_amdgcn_exp2f(m - base);
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] *= alpha;
+      m = mn;
+    }
+    Frag<E> p[4];  // tokens 8 (i % 2) + 0..7 of tile i / 2's granule
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[j][r], ks[j], -base));
+        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[j][r + 1], ks[j], -base));
+        l += p0 + p1;
+        p[2 * j + (r >> 3)].u[(r & 7) >> 1] = E::pack(p0, p1);
+      }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint4 v[2];
+      bool poisoned = false;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j] = *reinterpret_cast<const uint4*>(vb + 2048 * i + v_off[j]);
+        if (masked) {
+          const int vt = t0 + 32 * h + 16 * j;
+          const uint32_t bits = hide_codes(v[j], vid[j] < 0 ? 16 : any_lo - vt, any_hi - vt);
+          sh_nan[(wave * 32 + col) * 4 + 2 * h + j] = (uint16_t)bits;
+          poisoned = poisoned || __ballot(bits != 0) != 0;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        acc[i] = E::mfma32(dec8<E>(v[j].x, v[j].y, vs[j]), p[2 * j].v, acc[i]);
+        acc[i] = E::mfma32(dec8<E>(v[j].z, v[j].w, vs[j]), p[2 * j + 1].v, acc[i]);
+      }
+      if (poisoned) {  // the rows that see a NaN get it
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+        const unsigned long long seen = seen_bits(row, t0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (nan_map(sh_nan + (wave * 32 + 8 * (r >> 2) + 4 * h + (r & 3)) * 4) & seen) acc[i][r] = __builtin_nanf("");
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
+
+  l += __shfl_xor(l, 32, 64);
+  if (row.i < 0) return;
+  if (parts == 1) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t out = (int64_t)(blk.rows.first + row.i);
+    uint16_t* yr = a.y + out * a.yt + (int64_t)row.head * a.yh;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<uint2*>(yr + 32 * i + 2 * r + 4 * h) = make_uint2(
+            E::pack(acc[i][r] * inv, acc[i][r + 1] * inv), E::pack(acc[i][r + 2] * inv, acc[i][r + 3] * inv));
+    if (h == 0 && a.lse) a.lse[out * a.q_heads + row.head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+  } else {
+    const int64_t slot = (((id * a.c.heads + kvh) * a.splits + blockIdx.y) * kBlock) + 32 * wave + col;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4*>(a.part_o + slot * D + 32 * i + 2 * r + 4 * h) =
+            make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
+    if (h == 0) {
+      a.part_ml[slot * 2] = m;
+      a.part_ml[slot * 2 + 1] = l;
+    }
+  }
+}
+
+// joins the parts of a block: a thread takes four elements of a row, the parts in order
+template <class E, int D>
+__global__ __launch_bounds__(256) void attn_prompt_join(Args a) {
+  constexpr int LANES = D / 4;
+  const int kvh = blockIdx.x % a.c.heads;
+  const int64_t id = blockIdx.x / a.c.heads;
+  Block blk;
+  if (!find_block(a, id, blk)) return;
+  const int parts = parts_of(a, kv::tiles_of(blk.range));
+  if (parts == 1) return;
+  const int i = blockIdx.y * 256 + threadIdx.x, r = i / LANES, d = 4 * (i % LANES);
+  const Row row = row_at(a, blk.r0 + r, kvh, blk.rows.n, blk.len, room_of(a.c));
+  if (row.i < 0) return;
+  const int64_t first = ((id * a.c.heads + kvh) * a.splits) * kBlock + r;
+  float M = -INFINITY;
+  for (int p = 0; p < parts; ++p) M = fmaxf(M, a.part_ml[(first + (int64_t)p * kBlock) * 2]);
+  const float base = M == -INFINITY ? 0.0f : M;
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, L = 0.0f;
+  for (int p = 0; p < parts; ++p) {
+    const int64_t at = first + (int64_t)p * kBlock;
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[at * 2] - base);
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + d);
+    L += f * a.part_ml[at * 2 + 1];
+    o[0] += f * v.x;
+    o[1] += f * v.y;
+    o[2] += f * v.z;
+    o[3] += f * v.w;
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int64_t out = (int64_t)(blk.rows.first + row.i);
+  uint16_t* yr = a.y + out * a.yt + (int64_t)row.head * a.yh;
+  *reinterpret_cast<uint2*>(yr + d) = make_uint2(E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv));
+  if (d == 0 && a.lse) a.lse[out * a.q_heads + row.head] = (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+template <class E, int D>
+hipError_t launch(const Args& a, hipStream_t s) {
+  static std::atomic<unsigned long long> raised{0};
+  hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(attn_prompt<E, D>), prompt_lds(D), raised);
+  if (e != hipSuccess) return e;
+  const unsigned blocks = (unsigned)(prompt_blocks(a.T, a.c.batch, a.group) * a.c.heads);
+  hipLaunchKernelGGL((attn_prompt<E, D>), dim3(blocks, (unsigned)a.splits), dim3(256),
+                     prompt_lds(D), s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((attn_prompt_join<E, D>), dim3(blocks, kBlock * D / 4 / 256), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t prompt_blocks(int64_t T, int64_t batch, int64_t group) { return T * group / kBlock + batch; }
+
+hipError_t launch_attn_prompt(bsq_dtype dt, const attn::Args& a, hipStream_t s) {
+  const bool half = dt == BSQ_FP16;
+  switch (a.c.dim) {
+    case 64: return half ? launch<Fp16, 64>(a, s) : launch<Bf16, 64>(a, s);
+    case 128: return half ? launch<Fp16, 128>(a, s) : launch<Bf16, 128>(a, s);
+    default: return half ? launch<Fp16, 256>(a, s) : launch<Bf16, 256>(a, s);
+  }
+}
+
+}  // namespace bsq

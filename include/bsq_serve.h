@@ -164,7 +164,7 @@ bsq_status bsq_kv_append(bsq_dtype dtype, const bsq_kv8_cache* cache, const int3
  *     or a softmax_scale that is not finite
  * A sequence with seq_lens[b] < n_b has negative positions: those rows see
  * nothing (with BSQ_ATTN_FULL they see all). Tokens past max_pages count as
- * absent. k_scale is used as given; of v_scale only the exponent is.
+ * absent. Scales have to be what bsq_kv_append writes, powers of two or 0.
  * Workspace: bsq_attention_kv8_workspace_bytes(...) bytes, 256-byte aligned, not
  * shared by calls that may overlap: partial results of sequences that are
  * split over workgroups; nothing in it needs clearing or survives the call.

@@ -107,9 +107,81 @@ void check_attention(const Cache& c, const std::vector<int32_t>& cu, int64_t T, 
   if (pieces > (int64_t)target + c.batch) fail("more pieces than the grid holds", pieces, target, c.batch, 0);
 }
 
+// One tile in LDS: every byte of the 64 tokens comes exactly once, the operand reads find what they name, and
+// the 16 lanes that a 16-byte read serves at once fall into different sixteenths of 256 bytes.
+void apart(const char* what, const std::vector<int>& at) {
+  std::set<int> slots;
+  for (int o : at) {
+    if (o % 16) fail(what, o, 0, 0, 0);
+    slots.insert(o / 16 % 16);
+  }
+  if (slots.size() != 16 || at.size() != 16) fail(what, (long)slots.size(), at[0], at[1], 0);
+}
+template <int D, Kind kind>
+void check_k_tile() {
+  std::vector<int> holds((size_t)(64 * D / 16), -1);  // piece of the tile (token * D / 16 + piece) at each 16 bytes
+  for (int n = 0; n < D / 16; ++n)
+    for (int lane = 0; lane < 64; ++lane) {
+      const int gran = n / (D / 64), i = n % (D / 64);
+      // as the loads form it: granule 0's offset with the granule's exchange on top
+      const int src = k_source<D, kind>(i, 0, lane) ^ (16 * k_flip<D, kind>(16 * gran));
+      if (src != k_source<D, kind>(i, gran, lane)) fail("granule exchange", D, kind, n, lane);
+      if (src < 0 || src + 16 > 16 * D) fail("source outside the granule", D, kind, n, lane);
+      holds[(size_t)(64 * n + lane)] = gran * D + src / 16;
+      ++g_checked;
+    }
+  for (int token = 0; token < 64; ++token)
+    for (int piece = 0; piece < D / 16; ++piece) {
+      const int at = k_at<D, kind>(token, piece);
+      if (holds[(size_t)(at / 16)] != token * (D / 16) + piece) fail("K read finds another piece", D, kind, token, piece);
+    }
+  for (int piece = 0; piece < D / 16; ++piece)
+    for (int j = 0; j < 4; ++j) {
+      std::vector<int> at;
+      for (int l = 0; l < 16; ++l) {
+        if (kind == kStep) at.push_back(k_at<D, kind>(16 * (l >> 2) + 4 * j + (l & 3), piece));
+        else {  // lanes 16 (j % 2) .. + 15 of tile j / 2
+          const int c = l + 16 * (j & 1);
+          at.push_back(k_at<D, kind>(32 * (c >> 2 & 1) + 16 * (j >> 1) + 4 * (c >> 3) + (c & 3), piece));
+        }
+      }
+      apart("K bank conflict", at);
+    }
+}
+void check_v_tile() {
+  for (int page : {16, 32, 64, 128, 256}) {
+    const int gp = v_run(page);
+    std::vector<int> seen(64, 0);
+    for (int lane = 0; lane < 64; ++lane) {
+      const VSource v = v_source(lane, gp);
+      if (v.gran < 0 || v.gran > 3 || v.col < 0 || v.col > 15) fail("V source", page, lane, v.gran, v.col);
+      seen[(size_t)(16 * v.gran + v.col)]++;
+      for (int blk = 0; blk < 16; ++blk)
+        if (v_at(16 * blk + v.col, v.gran, gp) != 1024 * blk + 16 * lane) fail("V read finds another piece", page, lane, blk, 0);
+    }
+    for (int s : seen)
+      if (s != 1) fail("V piece not fetched once", page, s, 0, 0);
+    for (int g = 0; g < 4; ++g) {
+      std::vector<int> at;
+      for (int c = 0; c < 16; ++c) at.push_back(v_at(c, g, gp));
+      apart("V bank conflict", at);
+    }
+    // a tile's granules lie in pages as v_run says
+    for (int g = 0; g < 4; ++g)
+      if (page >= 64 ? (16 * g & (page - 1)) != 16 * g : (16 * g & (page - 1)) != 16 * (g % gp)) fail("V run", page, g, gp, 0);
+  }
+}
+
 }  // namespace
 
 int main() {
+  check_k_tile<64, kStep>();
+  check_k_tile<128, kStep>();
+  check_k_tile<256, kStep>();
+  check_k_tile<64, kPrompt>();
+  check_k_tile<128, kPrompt>();
+  check_k_tile<256, kPrompt>();
+  check_v_tile();
   std::mt19937 rng(1);
   auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
   for (int round = 0; round < 1500; ++round) {

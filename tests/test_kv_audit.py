@@ -34,6 +34,9 @@ def test_every_page_and_piece_is_in_bounds(tmp_path):
     ("(tiles - 1) / chunk + 1;", "(tiles + chunk - 1) / chunk;"),                             # wraps for one piece
     ("lo = lo / kTile * kTile;", ""),
     ("if (hi > room) hi = room;", ""),
+    ("if (D == 64) return gran;", "if (D == 64) return token & 3;"),                          # a bank conflict
+    ("return token * D + 16 * (piece ^ k_flip<D, kind>(token));", "return token * D + 16 * piece;"),
+    ("c * gp + ((g % gp) ^ (c * gp >> 4))", "c * gp + g % gp"),
 ])
 def test_planted_mistakes_are_found(tmp_path, old, new):
     src = open(os.path.join(CSRC, "kv_index.hpp")).read()
