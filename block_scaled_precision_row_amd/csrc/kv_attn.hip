@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
 #pragma unroll
     for (int s = 0; s < D / 32; ++s)
       q[s].q = row.i < 0 ? make_uint4(0, 0, 0, 0)
-                         : negated<E>(*reinterpret_cast<const uint4*>(qr + 64 * (s >> 1) + 16 * g + 8 * (s & 1)), a.flip);
+                         : signed_query(*reinterpret_cast<const uint4*>(qr + 64 * (s >> 1) + 16 * g + 8 * (s & 1)), a.sign);
   }
   int k_off[4];  // K tile j: this lane's row
 #pragma unroll
@@ -192,10 +192,9 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
     for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float mn = fmaxf(m, top);
-    const float base = mn == -INFINITY ? 0.0f : mn;
-    if (__ballot(mn != m)) {
-      const float alpha = __builtin_amdgcn_exp2f(m - base);
+    if (__ballot(outgrown(top, m))) {
+      const float mn = fmaxf(m, top);
+      const float alpha = __builtin_amdgcn_exp2f(m - finite_base(mn));
       l *= alpha;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -203,6 +202,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
         for (int r = 0; r < 4; ++r) acc[i][r] *= alpha;
       m = mn;
     }
+    const float base = finite_base(m);
     Frag<E> p[2];
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      uint4 v = *reinterpret_cast<const uint4*>(vb + 1024 * i + v_off);
+      v4u v = *reinterpret_cast<const v4u*>(vb + 1024 * i + v_off);
       bool poisoned = false;
       if (masked) {
         const uint32_t bits = hide_codes(v, vid < 0 ? 16 : any_lo - vt, any_hi - vt);
@@ -355,8 +355,9 @@ __global__ __launch_bounds__(256) void attn_join(Args a) {
 }
 
 // How a call is cut. Sequences of at most 16 rows (tokens times group) go to the step kernel, longer ones
-// to the prompt kernel; where max_q_len rules one of them out it is not launched, and a single
-// sequence goes to the prompt kernel whole.
+// to the prompt kernel. Where max_q_len rules one of them out it is not launched; where sequences have 256
+// rows and more on average, the few short ones that may be among them go to the prompt kernel too (an
+// idle step kernel and its join cost 9 us).
 struct Plan {
   bool step, prompt;
   int target;        // step: pieces wanted
@@ -369,7 +370,7 @@ Plan plan_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t
   Plan p{};
   const int64_t most = (max_q_len < T ? max_q_len : T) * group;
   p.prompt = most > 16;
-  p.step = most <= 16 || (batch > 1 && group <= 16);
+  p.step = most <= 16 || (group <= 16 && T < 256 * batch);
   if (p.step) {
     p.target = (int)((512 + kv_heads - 1) / kv_heads);
     p.pieces = p.target + batch;
@@ -414,8 +415,8 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.lse = p.lse;
   a.q_heads = p.q_heads;
   a.group = p.q_heads / p.c.heads;
-  a.flip = p.scale < 0.0f;
-  a.scale2 = (a.flip ? -p.scale : p.scale) * 1.44269504088896340736f;
+  a.sign = p.scale < 0.0f ? -1 : (p.scale > 0.0f ? 1 : 0);
+  a.scale2 = a.sign == 0 ? 1.0f : (a.sign < 0 ? -p.scale : p.scale) * 1.44269504088896340736f;
   a.window = p.window;
   a.full = p.full;
   a.max_q_len = (int)(p.max_q_len < p.T ? p.max_q_len : p.T);

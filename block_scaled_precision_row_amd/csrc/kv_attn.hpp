@@ -19,10 +19,10 @@ struct Args {
   float* lse;
   int64_t qt, qh, yt, yh;
   int q_heads, group;
-  float scale2;  // softmax_scale * log2(e)
+  float scale2;  // |softmax_scale| * log2(e)
   int64_t window;
   bool full;
-  bool flip;            // a negative softmax_scale: scale2 is its magnitude and q enters negated
+  int sign;             // of softmax_scale: q enters with it, scale2 is the magnitude (1 where it is 0)
   int max_q_len;
   int small;            // most rows (tokens times group) of a sequence that the step kernel takes
   int target, least;    // step kernel: pieces of all sequences together, least tiles of a piece
@@ -117,14 +117,16 @@ __device__ __forceinline__ void wait_loads() {  // until at most n vector-memory
 struct Pages {
   int id;
   float ks, vs;
-  // tile i starts at token t0 + stride * i; tokens from `end` on are not looked up
-  __device__ __forceinline__ void load(const Cache& c, int b, int head, int t0, int stride, int end) {
+  // tile i starts at token t0 + stride * i; tokens from `end` on are not looked up. Returns whether a page of
+  // those before it is absent.
+  __device__ __forceinline__ bool load(const Cache& c, int b, int head, int t0, int stride, int end) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)t0 + (int64_t)stride * (lane >> 2) + 16 * (lane & 3);
     id = t < end ? kv::page_of(c, b, (int)t) : -1;
     const int64_t at = (int64_t)(id < 0 ? 0 : id) * c.heads + head;
     ks = c.ks[at];
     vs = c.vs[at];
+    return __ballot(t < end && id < 0) != 0;
   }
   __device__ __forceinline__ int page(int tile, int gran) const { return __shfl(id, (tile & 15) * 4 + gran, 64); }
   __device__ __forceinline__ float kscale(int tile, int gran) const { return __shfl(ks, (tile & 15) * 4 + gran, 64); }
@@ -169,8 +171,7 @@ struct TileLoads {
 
 // Hides tokens of a lane's 16 V codes: bytes outside [lo, hi) become 0. NaN codes among the others become 0
 // too and are returned as bits (a row that does not see such a token must not meet it as 0 * NaN).
-__device__ __forceinline__ uint32_t hide_codes(uint4& v, int lo, int hi) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+__device__ __forceinline__ uint32_t hide_codes(v4u& w, int lo, int hi) {
   uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -190,10 +191,17 @@ __device__ __forceinline__ unsigned long long seen_bits(const Row& row, int t0) 
   return s;
 }
 
-template <class E>
-__device__ __forceinline__ uint4 negated(uint4 q, bool flip) {
-  const uint32_t m = flip ? 0x80008000u : 0u;
-  return make_uint4(q.x ^ m, q.y ^ m, q.z ^ m, q.w ^ m);
+// The maximum that probabilities are taken against may lag behind the scores' by 2^8: they are then at most 256
+// (the same relative precision in 16 bits, and far from overflow in fp32 sums), and most tiles need no
+// rescaling of what is summed up.
+__device__ __forceinline__ bool outgrown(float top, float m) { return top > m + 8.0f; }
+// (a row that has seen nothing has -inf: its probabilities exp2(-inf - 0) are 0)
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// eight query values with the softmax scale's sign (0: all zero)
+__device__ __forceinline__ uint4 signed_query(uint4 q, int sign) {
+  const uint32_t flip = sign < 0 ? 0x80008000u : 0u, keep = sign == 0 ? 0u : 0xFFFFFFFFu;
+  return make_uint4((q.x ^ flip) & keep, (q.y ^ flip) & keep, (q.z ^ flip) & keep, (q.w ^ flip) & keep);
 }
 
 }  // namespace attn

@@ -10,6 +10,8 @@
 // Bound by the matrix cores and, as near, by the vector instructions of the softmax and the decoding of E4M3
 // (two values an instruction). Tiles come into two LDS buffers, one in flight while the other is
 // worked on, with one barrier a tile.
+#include <type_traits>
+
 #include "kv_attn.hpp"
 
 namespace bsq {
@@ -41,16 +43,6 @@ __device__ __forceinline__ int block_sequence(const Args& a, int64_t id) {
   }
 }
 
-__device__ __forceinline__ int min32(int v) {  // over the 32 columns
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const int o = __shfl_xor(v, off, 64);
-    v = o < v ? o : v;
-  }
-  return __builtin_amdgcn_readfirstlane(v);
-}
-__device__ __forceinline__ int max32(int v) { return -min32(-v); }
-
 // a block's rows and the tokens they see
 struct Block {
   int b, r0;  // sequence, first row of its n * group
@@ -79,12 +71,12 @@ __device__ __forceinline__ int parts_of(const Args& a, int tiles) {
   return a.splits < most ? a.splits : most;
 }
 
-constexpr int prompt_lds(int D) { return 2 * tile_bytes(D) + 4 * 32 * 8; }  // buffers; the waves' NaN maps
+constexpr int prompt_lds(int D) { return 2 * tile_bytes(D) + D * 8; }  // buffers; the NaN map
 
 template <class E, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt(Args a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  uint16_t* sh_nan = reinterpret_cast<uint16_t*>(smem + 2 * tile_bytes(D));  // [wave][32 elements][4 granules]
+  uint16_t* sh_nan = reinterpret_cast<uint16_t*>(smem + 2 * tile_bytes(D));  // [D][4 granules]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, h = lane >> 5;
   // later blocks see more tokens: they go first; neighbouring workgroups, which go to different XCDs, take
@@ -116,15 +108,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt(Args a) {
 
   const int R = blk.r0 + 32 * wave + col;
   const Row row = row_at(a, R, kvh, blk.rows.n, blk.len, room);
-  const int any_lo = min32(row.i < 0 ? 0x7FFFFFFF : row.lo), any_hi = max32(row.i < 0 ? 0 : row.hi);
-  const int all_lo = max32(row.i < 0 ? 0 : row.lo), all_hi = min32(row.hi);
   Frag<E> q[D / 16];  // elements 32 (s / 2) + 16 h + 8 (s % 2) + 0..7
   {
     const uint16_t* qr = a.q + (int64_t)(blk.rows.first + (row.i < 0 ? 0 : row.i)) * a.qt + (int64_t)row.head * a.qh;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
       q[s].q = row.i < 0 ? make_uint4(0, 0, 0, 0)
-                         : negated<E>(*reinterpret_cast<const uint4*>(qr + 32 * (s >> 1) + 16 * h + 8 * (s & 1)), a.flip);
+                         : signed_query(*reinterpret_cast<const uint4*>(qr + 32 * (s >> 1) + 16 * h + 8 * (s & 1)), a.sign);
   }
   const int k_token = 32 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);  // K tile 0's row; tile 1's is 16 on
   const int gp = kv::v_run(1 << a.c.shift);
@@ -139,10 +129,58 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt(Args a) {
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
   float m = -INFINITY, l = 0.0f;
 
-  for (int it = 0; it < count; ++it) {
-    const int t0 = first + kv::kTile * it;
-    int vid[2];
-    float ks[2], vs[2];
+  // Granules j and 2 + j of a tile; `masked`: some row of the block does not see some of the tile.
+  auto half_tile = [&](auto masked, int j, int t0, const uint8_t* kb, int vid, float ks, float vs)
+                       __attribute__((always_inline)) {
+    const uint8_t* vb = kb + 64 * D;
+    v16f s;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 k = *reinterpret_cast<const uint4*>(kb + kv::k_at<D, kv::kPrompt>(k_token + 16 * j, 2 * i + h));
+      s = E::mfma32(dec8<E>(k.x, k.y, 1.0f), q[2 * i].v, s);
+      s = E::mfma32(dec8<E>(k.z, k.w, 1.0f), q[2 * i + 1].v, s);
+    }
+    if constexpr (masked) {
+      const int vt = t0 + 32 * h + 16 * j, lo = vid < 0 ? 16 : row.lo - vt, hi = row.hi - vt;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = r >= lo && r < hi ? s[r] * ks : -INFINITY;
+      ks = 1.0f;
+    }
+    float top = s[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+    top *= ks;
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    if (__ballot(outgrown(top, m))) {
+      const float mn = fmaxf(m, top);
+      const float alpha = __builtin_amdgcn_exp2f(m - finite_base(mn));
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] *= alpha;
+      m = mn;
+    }
+    const float base = finite_base(m);
+    Frag<E> p[2];  // tokens 8 i + 0..7 of the granule
+#pragma unroll
+    for (int r = 0; r < 16; r += 2) {
+      const float p0 = __builtin_amdgcn_exp2f(fmaf(s[r], ks, -base));
+      const float p1 = __builtin_amdgcn_exp2f(fmaf(s[r + 1], ks, -base));
+      l += p0 + p1;
+      p[r >> 3].u[(r & 7) >> 1] = E::pack(p0, p1);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(vb + 2048 * i + v_off[j]);
+      acc[i] = E::mfma32(dec8<E>(v.x, v.y, vs), p[0].v, acc[i]);
+      acc[i] = E::mfma32(dec8<E>(v.z, v.w, vs), p[1].v, acc[i]);
+    }
+  };
+  // waits for tile `it`, lets the next one start and gives the tile's pages and scales
+  auto advance = [&](int it, int t0, int(&vid)[2], float(&ks)[2], float(&vs)[2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       vid[j] = pages.page(it, 2 * h + j);
@@ -155,96 +193,80 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_prompt(Args a) {
       if (((it + 1) & 15) == 0) pages.load(a.c, blk.b, kvh, t0 + kv::kTile, kv::kTile, blk.range.hi);
       issue(it + 1, t0 + kv::kTile, lds + ((it + 1) & 1) * tile_bytes(D));
     }
-    if (t0 >= any_hi || t0 + kv::kTile <= any_lo) continue;  // nothing for this wave's rows
-    const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
-    const uint8_t* vb = kb + 64 * D;
-
-    v16f s[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[j][r] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 k = *reinterpret_cast<const uint4*>(kb + kv::k_at<D, kv::kPrompt>(k_token + 16 * j, 2 * i + h));
-        s[j] = E::mfma32(dec8<E>(k.x, k.y, 1.0f), q[2 * i].v, s[j]);
-        s[j] = E::mfma32(dec8<E>(k.z, k.w, 1.0f), q[2 * i + 1].v, s[j]);
+  };
+  // Tiles [whole_begin, whole_end), which all rows of the block see whole, run in a loop of their own, the others
+  // with the masks (one loop with a branch kept two copies of the accumulators: 250 registers spilled).
+  // With an absent page anywhere there are none.
+  int64_t last = (int64_t)blk.r0 + kBlock - 1;
+  const int64_t all = (int64_t)(blk.rows.n < a.max_q_len ? blk.rows.n : a.max_q_len) * a.group;
+  last = last < all ? last : all - 1;
+  const Row row0 = row_at(a, blk.r0, kvh, blk.rows.n, blk.len, room);
+  const Row row1 = row_at(a, (int)last, kvh, blk.rows.n, blk.len, room);
+  const int any_lo = row0.lo, any_hi = row1.hi;
+  int whole_begin = 0, whole_end = count;
+  {
+    bool absent = false;
+    const int end = first + kv::kTile * count < blk.range.hi ? first + kv::kTile * count : blk.range.hi;
+    for (int64_t t = (int64_t)first + 16 * lane; t < end; t += 1024) absent = absent || kv::page_of(a.c, blk.b, (int)t) < 0;
+    const int upto = row0.hi > first ? (row0.hi - first) / kv::kTile : 0;
+    if (row1.lo > first) whole_begin = (row1.lo - first + kv::kTile - 1) / kv::kTile;
+    whole_begin = whole_begin < count ? whole_begin : count;
+    whole_end = __ballot(absent) ? 0 : (upto < count ? upto : count);
+    whole_end = whole_end < whole_begin ? whole_begin : whole_end;
+    whole_begin = __builtin_amdgcn_readfirstlane(whole_begin);
+    whole_end = __builtin_amdgcn_readfirstlane(whole_end);
+  }
+  uint32_t bad[(D + 63) / 64] = {};  // accumulators (by number) whose row has seen a NaN of V
+  auto masked_tiles = [&](int from, int to) __attribute__((always_inline)) {
+    for (int it = from; it < to; ++it) {
+      const int t0 = first + kv::kTile * it;
+      const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
+      const int vgran = pages.page(it, loads.v_gran);
+      int vid[2];
+      float ks[2], vs[2];
+      advance(it, t0, vid, ks, vs);
+      // V's codes that no row sees, and NaN codes, become 0 in LDS (a probability of 0 must not meet them); which
+      // were NaN is kept for the rows that see them
+      uint32_t found = 0;
+      for (int n = wave; n < D / 16; n += 4) {
+        v4u* at = reinterpret_cast<v4u*>(smem + (it & 1) * tile_bytes(D) + 64 * D + 1024 * n + 16 * lane);
+        v4u v = *at;
+        const int t = t0 + 16 * loads.v_gran;
+        const uint32_t bits = hide_codes(v, vgran < 0 ? 16 : any_lo - t, any_hi - t);
+        *at = v;
+        sh_nan[(16 * n + loads.v_col) * 4 + loads.v_gran] = (uint16_t)bits;
+        found |= bits;
       }
-    }
-    const bool masked = t0 < all_lo || t0 + kv::kTile > all_hi || __ballot(vid[0] < 0 || vid[1] < 0) != 0;
-    float top = -INFINITY;
-    if (masked) {
+      const bool poisoned = __syncthreads_or(found != 0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int vt = t0 + 32 * h + 16 * j, lo = vid[j] < 0 ? 16 : row.lo - vt, hi = row.hi - vt;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[j][r] = r >= lo && r < hi ? s[j][r] * ks[j] : -INFINITY;
-          top = fmaxf(top, s[j][r]);
-        }
-        ks[j] = 1.0f;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float t = s[j][0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) t = fmaxf(t, s[j][r]);
-        top = fmaxf(top, t * ks[j]);
-      }
-    }
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float mn = fmaxf(m, top);
-    const float base = mn == -INFINITY ? 0.0f : mn;
-    if (__ballot(mn != m)) {
-      const float alpha = __builtin_amdgcn_exp2f(m - base);
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][r] *= alpha;
-      m = mn;
-    }
-    Frag<E> p[4];  // tokens 8 (i % 2) + 0..7 of tile i / 2's granule
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; r += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[j][r], ks[j], -base));
-        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[j][r + 1], ks[j], -base));
-        l += p0 + p1;
-        p[2 * j + (r >> 3)].u[(r & 7) >> 1] = E::pack(p0, p1);
-      }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint4 v[2];
-      bool poisoned = false;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        v[j] = *reinterpret_cast<const uint4*>(vb + 2048 * i + v_off[j]);
-        if (masked) {
-          const int vt = t0 + 32 * h + 16 * j;
-          const uint32_t bits = hide_codes(v[j], vid[j] < 0 ? 16 : any_lo - vt, any_hi - vt);
-          sh_nan[(wave * 32 + col) * 4 + 2 * h + j] = (uint16_t)bits;
-          poisoned = poisoned || __ballot(bits != 0) != 0;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        acc[i] = E::mfma32(dec8<E>(v[j].x, v[j].y, vs[j]), p[2 * j].v, acc[i]);
-        acc[i] = E::mfma32(dec8<E>(v[j].z, v[j].w, vs[j]), p[2 * j + 1].v, acc[i]);
-      }
-      if (poisoned) {  // the rows that see a NaN get it
-        __threadfence_block();
-        __builtin_amdgcn_wave_barrier();
+      for (int j = 0; j < 2; ++j) half_tile(std::true_type(), j, t0, kb, vid[j], ks[j], vs[j]);
+      if (poisoned) {
         const unsigned long long seen = seen_bits(row, t0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (nan_map(sh_nan + (wave * 32 + 8 * (r >> 2) + 4 * h + (r & 3)) * 4) & seen) acc[i][r] = __builtin_nanf("");
-        __builtin_amdgcn_wave_barrier();
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (nan_map(sh_nan + (32 * i + 8 * (r >> 2) + 4 * h + (r & 3)) * 4) & seen)
+              bad[i >> 1] |= 1u << (16 * (i & 1) + r);
       }
     }
+  };
+  masked_tiles(0, whole_begin);
+  for (int it = whole_begin; it < whole_end; ++it) {
+    const int t0 = first + kv::kTile * it;
+    const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
+    int vid[2];
+    float ks[2], vs[2];
+    advance(it, t0, vid, ks, vs);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) half_tile(std::false_type(), j, t0, kb, vid[j], ks[j], vs[j]);
   }
+  masked_tiles(whole_end, count);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (bad[i >> 1] >> (16 * (i & 1) + r) & 1) acc[i][r] = __builtin_nanf("");
 
   l += __shfl_xor(l, 32, 64);
   if (row.i < 0) return;
