@@ -46,42 +46,53 @@ __device__ __forceinline__ int sequence_tiles(const Args& a, int b) {
   return kv::tiles_of(kv::seen_range(len < 0 ? 0 : len, room_of(a.c), n, 0, n, a.window, a.full));
 }
 
-// Which part of which sequence a workgroup takes. Every wave finds it by itself from the lengths:
-// a sum over the sequences gives the piece size, a prefix sum of their pieces the sequence. So the
-// host needs to know no length, and a batch of any raggedness is cut into equal pieces.
-struct Piece {
-  int b, index, count;
+// The tiles of all sequences together. Every wave finds sums and places by itself from the lengths, 64
+// sequences at a time.
+struct Tiles {
+  int64_t total;
+  int ranges;
+  int mine, upto;  // this lane's sequence (batches of up to 64) and the sum up to it
 };
-__device__ __forceinline__ int plan_chunk(const Args& a) {
+__device__ __forceinline__ int lane_tiles(const Args& a, int b) {
+  const int t = b < a.c.batch ? sequence_tiles(a, b) : 0;
+  return t > 0 ? t : 0;
+}
+__device__ __forceinline__ Tiles count_tiles(const Args& a) {
   const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.c.batch; b0 += 64) {
-    const int t = b0 + lane < a.c.batch ? sequence_tiles(a, b0 + lane) : 0;
-    total += wave_sum(t > 0 ? t : 0);
-  }
-  return kv::chunk_of(total, a.target, a.least);
+  Tiles t;
+  t.mine = lane_tiles(a, lane);
+  t.upto = wave_scan(t.mine);
+  t.total = __builtin_amdgcn_readfirstlane(__shfl(t.upto, 63, 64));
+  for (int b0 = 64; b0 < a.c.batch; b0 += 64) t.total += __builtin_amdgcn_readfirstlane(wave_sum(lane_tiles(a, b0 + lane)));
+  t.ranges = kv::ranges_of(t.total, a.target, a.least);
+  return t;
 }
-__device__ __forceinline__ int piece_count(const Args& a, int b, int chunk) {
-  const int t = sequence_tiles(a, b);
-  return t < 0 ? 0 : kv::pieces_of(t, chunk);
-}
-__device__ __forceinline__ bool find_piece(const Args& a, int id, Piece& out) {
-  const int lane = threadIdx.x & 63, chunk = plan_chunk(a);
-  int before = 0;
-  for (int b0 = 0; b0 < a.c.batch; b0 += 64) {
-    const int n = b0 + lane < a.c.batch ? piece_count(a, b0 + lane, chunk) : 0;
-    const int upto = before + wave_scan(n);
-    const unsigned long long hit = __ballot(upto > id);
-    if (hit) {
-      const int at = __builtin_ctzll(hit);
-      out.b = __builtin_amdgcn_readfirstlane(b0 + at);
-      out.count = __builtin_amdgcn_readfirstlane(__shfl(n, at, 64));
-      out.index = __builtin_amdgcn_readfirstlane(id - __shfl(upto - n, at, 64));
-      return true;
+// the sequence that holds tile x and the number of its tiles before x
+__device__ __forceinline__ void find_tile(const Args& a, const Tiles& t, int64_t x, int& b, int& before) {
+  const int lane = threadIdx.x & 63;
+  int64_t sum = 0;
+  int mine = t.mine, upto = t.upto;
+  for (int b0 = 0;; b0 += 64) {
+    if (b0 > 0) {
+      mine = lane_tiles(a, b0 + lane);
+      upto = wave_scan(mine);
     }
-    before = __shfl(upto, 63, 64);
+    const unsigned long long hit = __ballot(sum + upto > x);
+    if (hit || b0 + 64 >= a.c.batch) {
+      const int at = hit ? __builtin_ctzll(hit) : 63;
+      b = __builtin_amdgcn_readfirstlane(b0 + at);
+      before = __builtin_amdgcn_readfirstlane((int)(x - sum) - __shfl(upto - mine, at, 64));
+      return;
+    }
+    sum += __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
   }
-  return false;
+}
+// tiles of the sequences before b
+__device__ __forceinline__ int64_t tiles_before(const Args& a, int b) {
+  const int lane = threadIdx.x & 63;
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < b; b0 += 64) sum += wave_sum(b0 + lane < b ? lane_tiles(a, b0 + lane) : 0);
+  return sum;
 }
 
 __device__ __forceinline__ int min16(int v) {  // over the 16 columns
@@ -108,23 +119,35 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
   uint16_t* sh_nan = reinterpret_cast<uint16_t*>(sh_ml + W * 16 * 2);       // [W][D][4 granules]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int kvh = blockIdx.y;
-  Piece pc;
-  if (!find_piece(a, blockIdx.x, pc)) return;
-  const int b = pc.b, pieces = pc.count;
+  const int kvh = blockIdx.y, room = room_of(a.c), range = blockIdx.x;
+  const Tiles plan = count_tiles(a);
+  if (plan.total == 0 || range >= plan.ranges) return;
+  const int64_t begin = kv::range_begin(plan.total, plan.ranges, range);
+  const int64_t end = kv::range_begin(plan.total, plan.ranges, range + 1);
+  const TileLoads<D, kv::kStep> loads(a.c);
+  const int gp = kv::v_run(1 << a.c.shift);
+  const int v_off = kv::v_at(col, g, gp);
+  int k_off[4];  // K tile j: this lane's row
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k_off[j] = 16 * (col >> 2) + 4 * j + (col & 3);
+
+  for (int64_t x0 = begin; x0 < end;) {  // the sequences of the range
+  int b, tile0;
+  find_tile(a, plan, x0, b, tile0);
   const kv::Rows rows = kv::rows_of(a.cu, b, a.T);
-  const int room = room_of(a.c);
   int len = a.c.lens[b];
   len = len < 0 ? 0 : len;
   const kv::Range all = kv::seen_range(len, room, rows.n, 0, rows.n, a.window, a.full);
   const int tiles = kv::tiles_of(all);
-  const int tile0 = kv::piece_begin(tiles, pieces, pc.index), tile1 = kv::piece_begin(tiles, pieces, pc.index + 1);
+  const int tile1 = end - x0 < tiles - tile0 ? tile0 + (int)(end - x0) : tiles;
+  const bool direct = tile0 == 0 && tile1 == tiles;
+  const int64_t part = kv::partial_slot(range, x0 == begin);
+  x0 += tile1 - tile0;
   const int count = tile1 - tile0 - wave > 0 ? (tile1 - tile0 - wave + W - 1) / W : 0;  // this wave's tiles
   const int first = all.lo + kv::kTile * (tile0 + wave), stride = kv::kTile * W;
 
   const uint8_t* buf = smem + wave * 2 * tile_bytes(D);
   const uint32_t buf_lds = lds_offset(buf);
-  const TileLoads<D, kv::kStep> loads(a.c);
   Pages pages;
   if (count > 0) {
     pages.load(a.c, b, kvh, first, stride, all.hi);
@@ -142,11 +165,6 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
       q[s].q = row.i < 0 ? make_uint4(0, 0, 0, 0)
                          : signed_query(*reinterpret_cast<const uint4*>(qr + 64 * (s >> 1) + 16 * g + 8 * (s & 1)), a.sign);
   }
-  int k_off[4];  // K tile j: this lane's row
-#pragma unroll
-  for (int j = 0; j < 4; ++j) k_off[j] = 16 * (col >> 2) + 4 * j + (col & 3);
-  const int gp = kv::v_run(1 << a.c.shift);
-  const int v_off = kv::v_at(col, g, gp);
 
   v4f acc[D / 16];
 #pragma unroll
@@ -261,7 +279,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
       f[w] = __builtin_amdgcn_exp2f(sh_ml[(w * 16 + jr) * 2] - base);
       L += f[w] * sh_ml[(w * 16 + jr) * 2 + 1];
     }
-    const int64_t slot = ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * 16 + jr;
+    const int64_t slot = (part * a.c.heads + kvh) * 16 + jr;
     const int64_t out = (int64_t)(rows.first + jrow.i);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
@@ -275,7 +293,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
         o[2] += f[w] * v.z;
         o[3] += f[w] * v.w;
       }
-      if (pieces == 1) {
+      if (direct) {
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         uint16_t* yr = a.y + out * a.yt + (int64_t)jrow.head * a.yh;
         *reinterpret_cast<uint2*>(yr + d) = make_uint2(E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv));
@@ -284,7 +302,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
       }
     }
     if (jd == 0) {
-      if (pieces == 1) {
+      if (direct) {
         if (a.lse) a.lse[out * a.q_heads + jrow.head] = (M + __builtin_amdgcn_logf(L)) * kLn2;
       } else {
         a.part_ml[slot * 2] = M;
@@ -292,41 +310,51 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
       }
     }
   }
+  __syncthreads();  // the results are read before the next sequence's tiles arrive in their place
+  }
 }
 
-// joins the pieces of a sequence that was split: a workgroup per row (sequence, kv head, row of
-// its 16), the pieces in a fixed order
+// Joins the partial results of a sequence that lies in several ranges, in their order, and writes the rows of
+// one without tokens: a workgroup per row (sequence, kv head, row of its 16).
 template <class E, int D>
-__global__ __launch_bounds__(256) void attn_join(Args a) {
-  constexpr int LANES = D / 4, PER = 256 / LANES;  // threads over the elements, pieces at a time
+__global__ __launch_bounds__(256) void attn_join(Args a, int rows_max) {
+  constexpr int LANES = D / 4, PER = 256 / LANES;  // threads over the elements, partial results at a time
   __shared__ float sh[PER][D + 4];
   __shared__ float sh_l[PER];
-  const int b = blockIdx.x, kvh = blockIdx.y / 16, R = blockIdx.y % 16;
+  const int b = blockIdx.x, kvh = blockIdx.y / rows_max, R = blockIdx.y % rows_max;
   const kv::Rows rows = kv::rows_of(a.cu, b, a.T);
-  if (R >= rows.n * a.group) return;
+  const int tiles = sequence_tiles(a, b);
+  if (tiles < 0) return;
   int len = a.c.lens[b];
   len = len < 0 ? 0 : len;
   const Row row = row_at(a, R, kvh, rows.n, len, room_of(a.c));
   if (row.i < 0) return;
-  const int chunk = plan_chunk(a);
-  const int pieces = piece_count(a, b, chunk);
-  if (pieces <= 1) return;
-  int before = 0;
-  const int lane = threadIdx.x & 63;
-  for (int b0 = 0; b0 < b; b0 += 64) before += wave_sum(b0 + lane < b ? piece_count(a, b0 + lane, chunk) : 0);
-  const int64_t stride = (int64_t)a.c.heads * 16;  // rows of one piece
-  const int64_t first = ((int64_t)before * a.c.heads + kvh) * 16 + R;
-  float M = -INFINITY;
-  for (int i = lane; i < pieces; i += 64) M = fmaxf(M, a.part_ml[(first + i * stride) * 2]);
-  M = wave_max(M);
-  const float base = M == -INFINITY ? 0.0f : M;
   const int who = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
+  uint16_t* yr = a.y + (int64_t)(rows.first + row.i) * a.yt + (int64_t)row.head * a.yh;
+  float* lse = a.lse ? a.lse + (int64_t)(rows.first + row.i) * a.q_heads + row.head : nullptr;
+  if (tiles == 0) {
+    if (who == 0) *reinterpret_cast<uint2*>(yr + d) = make_uint2(0, 0);
+    if (threadIdx.x == 0 && lse) *lse = -INFINITY;
+    return;
+  }
+  const Tiles plan = count_tiles(a);
+  const int64_t x = tiles_before(a, b);
+  const int r0 = kv::range_of(plan.total, plan.ranges, x), r1 = kv::range_of(plan.total, plan.ranges, x + tiles - 1);
+  if (r0 == r1) return;
+  const int pieces = r1 - r0 + 1;
+  const bool first_begins = x == kv::range_begin(plan.total, plan.ranges, r0);
+  auto at = [&](int i) { return (kv::partial_slot(r0 + i, i > 0 || first_begins) * a.c.heads + kvh) * 16 + R; };
+  float M = -INFINITY;
+  for (int i = threadIdx.x & 63; i < pieces; i += 64) M = fmaxf(M, a.part_ml[at(i) * 2]);
+  M = wave_max(M);
+  const float base = finite_base(M);
   float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, L = 0.0f;
+#pragma unroll 4
   for (int i = who; i < pieces; i += PER) {
-    const int64_t at = first + i * stride;
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[at * 2] - base);
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + d);
-    L += f * a.part_ml[at * 2 + 1];
+    const int64_t p = at(i);
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[p * 2] - base);
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + p * D + d);
+    L += f * a.part_ml[p * 2 + 1];
     o[0] += f * v.x;
     o[1] += f * v.y;
     o[2] += f * v.z;
@@ -348,33 +376,31 @@ __global__ __launch_bounds__(256) void attn_join(Args a) {
 #pragma unroll
   for (int w = 1; w < PER; ++w) L += sh_l[w];
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  uint16_t* yr = a.y + (int64_t)(rows.first + row.i) * a.yt + (int64_t)row.head * a.yh;
   *reinterpret_cast<uint2*>(yr + d) = make_uint2(E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv));
-  if (d == 0 && a.lse)
-    a.lse[(int64_t)(rows.first + row.i) * a.q_heads + row.head] = (M + __builtin_amdgcn_logf(L)) * kLn2;
+  if (d == 0 && lse) *lse = (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
 // How a call is cut. Sequences of at most 16 rows (tokens times group) go to the step kernel, longer ones
 // to the prompt kernel. Where max_q_len rules one of them out it is not launched; where sequences have 256
 // rows and more on average, the few short ones that may be among them go to the prompt kernel too (an
 // idle step kernel and its join cost 9 us).
-struct Plan {
+struct Cut {
   bool step, prompt;
-  int target;        // step: pieces wanted
-  int64_t pieces;    // step: most pieces
+  int target;        // step: most ranges
+  int rows;          // step: most rows of a sequence and kv head
   int64_t blocks;    // prompt: most blocks of 128 rows
   int splits;
   size_t step_bytes, prompt_bytes;
 };
-Plan plan_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t kv_heads, int64_t D) {
-  Plan p{};
+Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t kv_heads, int64_t D) {
+  Cut p{};
   const int64_t most = (max_q_len < T ? max_q_len : T) * group;
   p.prompt = most > 16;
   p.step = most <= 16 || (group <= 16 && T < 256 * batch);
   if (p.step) {
-    p.target = (int)((512 + kv_heads - 1) / kv_heads);
-    p.pieces = p.target + batch;
-    p.step_bytes = (size_t)(p.pieces * kv_heads * 16 * (D + 2) * 4 + 255) & ~(size_t)255;
+    p.target = (int)((512 + kv_heads - 1) / kv_heads);  // two workgroups to a compute unit
+    p.rows = (int)(most < 16 ? most : 16);
+    p.step_bytes = (size_t)(2 * p.target * kv_heads * 16 * (D + 2) * 4 + 255) & ~(size_t)255;
   }
   if (p.prompt) {
     p.blocks = prompt_blocks(T, batch, group);
@@ -387,15 +413,16 @@ Plan plan_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t
 constexpr int kLeastTiles = 4;
 
 template <class E, int D>
-hipError_t launch_step(const Args& a, const Plan& p, hipStream_t s) {
+hipError_t launch_step(const Args& a, const Cut& p, hipStream_t s) {
   static std::atomic<unsigned long long> raised{0};
   hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(attn_step<E, D>), step_lds(D), raised);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_step<E, D>), dim3((unsigned)p.pieces, (unsigned)a.c.heads), dim3(64 * step_waves(D)),
+  hipLaunchKernelGGL((attn_step<E, D>), dim3((unsigned)p.target, (unsigned)a.c.heads), dim3(64 * step_waves(D)),
                      step_lds(D), s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_join<E, D>), dim3((unsigned)a.c.batch, (unsigned)a.c.heads * 16), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((attn_join<E, D>), dim3((unsigned)a.c.batch, (unsigned)(a.c.heads * p.rows)), dim3(256), 0, s, a,
+                     p.rows);
   return hipGetLastError();
 }
 
@@ -403,7 +430,7 @@ hipError_t launch_step(const Args& a, const Plan& p, hipStream_t s) {
 
 size_t attention_workspace(int64_t batch, int64_t T, int64_t max_q_len, int64_t q_heads, int64_t kv_heads,
                            int64_t head_dim) {
-  const Plan p = plan_of(batch, T, max_q_len, q_heads / kv_heads, kv_heads, head_dim);
+  const Cut p = cut_of(batch, T, max_q_len, q_heads / kv_heads, kv_heads, head_dim);
   return p.step_bytes + p.prompt_bytes;
 }
 
@@ -420,7 +447,7 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.window = p.window;
   a.full = p.full;
   a.max_q_len = (int)(p.max_q_len < p.T ? p.max_q_len : p.T);
-  const Plan plan = plan_of(p.c.batch, p.T, p.max_q_len, a.group, p.c.heads, p.c.dim);
+  const Cut plan = cut_of(p.c.batch, p.T, p.max_q_len, a.group, p.c.heads, p.c.dim);
   a.least = kLeastTiles;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   hipError_t e = hipSuccess;
@@ -436,7 +463,7 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.small = plan.prompt ? 16 : 0x7FFFFFFF;  // (a sequence longer than max_q_len promised is cut, not left out)
   a.target = plan.target;
   a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = a.part_o + plan.pieces * p.c.heads * 16 * p.c.dim;
+  a.part_ml = a.part_o + (int64_t)2 * plan.target * p.c.heads * 16 * p.c.dim;
   const bool half = dt == BSQ_FP16;
   switch (p.c.dim) {
     case 64: return half ? launch_step<Fp16, 64>(a, plan, s) : launch_step<Bf16, 64>(a, plan, s);

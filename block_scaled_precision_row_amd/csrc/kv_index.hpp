@@ -103,14 +103,21 @@ BSQ_HD Range seen_range(int len, int room, int n, int i0, int rows, int64_t wind
 }
 BSQ_HD int tiles_of(Range r) { return (r.hi - r.lo + kTile - 1) / kTile; }
 
-// A sequence of `tiles` tiles is cut into pieces of at most `chunk`, one workgroup each (an
-// empty one keeps one piece, which writes its rows' zeros). With chunk = max(least,
-// ceil(total / target)) all sequences together have at most target + batch pieces.
-BSQ_HD int chunk_of(int64_t total, int target, int least) {
-  const int64_t c = (total + target - 1) / target;
-  return (int)(c < least ? least : (c > 0x7FFFFFFF ? 0x7FFFFFFF : c));
+// The tiles of all sequences, one after the other, are cut into `ranges` equal runs, one to a workgroup, which
+// may end one sequence and begin another. So a batch of any raggedness keeps all workgroups equally long,
+// and the host needs to know no length.
+BSQ_HD int ranges_of(int64_t total, int target, int least) {
+  const int64_t r = total / least;
+  return (int)(r < 1 ? 1 : (r > target ? target : r));
 }
-BSQ_HD int pieces_of(int tiles, int chunk) { return tiles == 0 ? 1 : (tiles - 1) / chunk + 1; }
+BSQ_HD int64_t range_begin(int64_t total, int ranges, int r) { return total * r / ranges; }
+// the range that holds tile x: the last r with total * r / ranges <= x
+BSQ_HD int range_of(int64_t total, int ranges, int64_t x) { return (int)(((x + 1) * ranges - 1) / total); }
+// A sequence that lies in several ranges leaves a partial result in each: at most one range begins inside
+// it or with it (slot 2 r) for every one but the first, which may hold others before it (slot 2 r + 1).
+BSQ_HD int64_t partial_slot(int r, bool at_begin) { return 2 * (int64_t)r + (at_begin ? 0 : 1); }
+
+// A prompt block's tiles are cut into equal parts.
 BSQ_HD int piece_begin(int tiles, int pieces, int i) { return (int)((int64_t)tiles * i / pieces); }
 
 // ---- a tile of 64 tokens of one head in LDS ---------------------------------------------

@@ -3,8 +3,8 @@
 // addresses from, over regular batches and over lengths and tables out of every range.
 //  * append: the slots give every touched page of every sequence exactly once, each new token is
 //    in exactly one, and rows, page ids and places lie inside their tensors whatever is read;
-//  * attention: the tokens that rows see are covered by the pieces exactly once, the pieces of a
-//    batch number at most target + batch, and every page looked up is a page of the pool or absent.
+//  * attention: the tokens that rows see are covered by the ranges exactly once, partial results have slots of
+//    their own and are found again, and every page looked up is a page of the pool or absent.
 // Prints one line and exits with 1 on the first violation.
 #include <cstdio>
 #include <cstdlib>
@@ -86,25 +86,50 @@ void check_attention(const Cache& c, const std::vector<int32_t>& cu, int64_t T, 
     }
     total += tiles[b];
   }
-  const int chunk = target > 0 ? chunk_of(total, target, least) : 0x7FFFFFFF;
-  int64_t pieces = 0;
-  for (int b = 0; b < c.batch; ++b) {
-    if (tiles[b] < 0) continue;
-    const int p = pieces_of(tiles[b], chunk);
-    if (p < 1) fail("a sequence without a piece", b, p, tiles[b], chunk);
-    pieces += p;
-    if (piece_begin(tiles[b], p, 0) != 0 || piece_begin(tiles[b], p, p) != tiles[b]) fail("pieces do not cover", b, p, tiles[b], 0);
-    for (int i = 0; i < p; ++i) {
-      const int n = piece_begin(tiles[b], p, i + 1) - piece_begin(tiles[b], p, i);
-      if (n < 0 || n > chunk) fail("piece size", b, i, n, chunk);
-      ++g_checked;
-    }
-    for (int t = range[b].lo; t < range[b].hi && t < range[b].lo + 4096; t += 16) {
+  for (int b = 0; b < c.batch; ++b)
+    for (int t = range[b].lo; tiles[b] > 0 && t < range[b].hi && t < range[b].lo + 4096; t += 16) {
       const int id = page_of(c, b, t);
       if (id < -1 || id >= c.num_pages) fail("page outside the pool", b, t, id, 0);
     }
+  if (total == 0) return;
+  // the ranges as the workgroups walk them: every tile of every sequence once, partial results in slots of
+  // their own, and the joining looks for exactly those
+  const int ranges = ranges_of(total, target, least);
+  if (ranges < 1 || ranges > target || range_begin(total, ranges, 0) != 0 || range_begin(total, ranges, ranges) != total)
+    fail("ranges", ranges, target, total, 0);
+  std::vector<int64_t> before((size_t)c.batch + 1, 0);
+  for (int b = 0; b < c.batch; ++b) before[b + 1] = before[b] + (tiles[b] > 0 ? tiles[b] : 0);
+  std::set<int64_t> slots;
+  std::vector<std::set<int64_t>> left((size_t)c.batch);
+  std::vector<int64_t> done((size_t)c.batch, 0);
+  for (int r = 0; r < ranges; ++r) {
+    const int64_t begin = range_begin(total, ranges, r), end = range_begin(total, ranges, r + 1);
+    if (end - begin > (total + ranges - 1) / ranges + 1) fail("range size", r, end - begin, total, ranges);
+    for (int64_t x = begin; x < end;) {
+      int b = 0;
+      while (before[b + 1] <= x) ++b;
+      const int64_t t0 = x - before[b], t1 = end - x < tiles[b] - t0 ? t0 + (end - x) : tiles[b];
+      if (t0 != done[b] || t1 <= t0) fail("tiles not in turn", b, t0, t1, done[b]);
+      done[b] = t1;
+      if (!(t0 == 0 && t1 == tiles[b])) {
+        const int64_t s = partial_slot(r, x == begin);
+        if (s < 0 || s >= 2 * (int64_t)target || !slots.insert(s).second) fail("slot", b, r, s, 0);
+        left[b].insert(s);
+      }
+      if (range_of(total, ranges, x) != r || range_of(total, ranges, x + (t1 - t0) - 1) != r) fail("range of a tile", b, r, x, 0);
+      x += t1 - t0;
+      ++g_checked;
+    }
   }
-  if (pieces > (int64_t)target + c.batch) fail("more pieces than the grid holds", pieces, target, c.batch, 0);
+  for (int b = 0; b < c.batch; ++b) {
+    if (tiles[b] <= 0) continue;
+    if (done[b] != tiles[b]) fail("tiles left out", b, done[b], tiles[b], 0);
+    const int r0 = range_of(total, ranges, before[b]), r1 = range_of(total, ranges, before[b + 1] - 1);
+    std::set<int64_t> want;
+    if (r0 != r1)
+      for (int r = r0; r <= r1; ++r) want.insert(partial_slot(r, r > r0 || before[b] == range_begin(total, ranges, r0)));
+    if (want != left[b]) fail("the join looks elsewhere", b, r0, r1, (long)left[b].size());
+  }
 }
 
 // One tile in LDS: every byte of the 64 tokens comes exactly once, the operand reads find what they name, and
@@ -214,7 +239,7 @@ int main() {
     c.lens = lens.data();
     if (T > 0) check_append(c, cu, T, regular);
     for (int w = 0; w < 3; ++w)
-      check_attention(c, cu, T, w == 1 ? pick(1, 300) : 0, w == 2, pick(0, 3) ? pick(1, 600) : 0, pick(1, 8));
+      check_attention(c, cu, T, w == 1 ? pick(1, 300) : 0, w == 2, pick(1, 600), pick(1, 8));
   }
   std::printf("ok: %ld pages and pieces checked\n", g_checked);
   return 0;

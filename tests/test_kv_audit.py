@@ -30,8 +30,8 @@ def test_every_page_and_piece_is_in_bounds(tmp_path):
     ("+ 2 * (int64_t)b;", "+ (int64_t)b;"),                                                   # too few slots
     ("hi = hi < lo ? lo : (hi > t ? t : hi);", "hi = hi < lo ? lo : hi;"),                    # rows past T
     ("if (r.n == 0 || past < 0) return none;", "if (r.n == 0) return none;"),                 # a negative position
-    ("const int64_t c = (total + target - 1) / target;", "const int64_t c = total / target;"),  # too many pieces
-    ("(tiles - 1) / chunk + 1;", "(tiles + chunk - 1) / chunk;"),                             # wraps for one piece
+    ("return (int)(((x + 1) * ranges - 1) / total);", "return (int)(x * ranges / total);"),
+    ("2 * (int64_t)r + (at_begin ? 0 : 1)", "(int64_t)r"),
     ("lo = lo / kTile * kTile;", ""),
     ("if (hi > room) hi = room;", ""),
     ("if (D == 64) return gran;", "if (D == 64) return token & 3;"),                          # a bank conflict
