@@ -49,8 +49,7 @@ __device__ __forceinline__ int sequence_tiles(const Args& a, int b) {
 // The tiles of all sequences together. Every wave finds sums and places by itself from the lengths, 64
 // sequences at a time.
 struct Tiles {
-  int64_t total;
-  int ranges;
+  int total, chunk;
   int mine, upto;  // this lane's sequence (batches of up to 64) and the sum up to it
 };
 __device__ __forceinline__ int lane_tiles(const Args& a, int b) {
@@ -62,15 +61,15 @@ __device__ __forceinline__ Tiles count_tiles(const Args& a) {
   Tiles t;
   t.mine = lane_tiles(a, lane);
   t.upto = wave_scan(t.mine);
-  t.total = __builtin_amdgcn_readfirstlane(__shfl(t.upto, 63, 64));
+  t.total = __builtin_amdgcn_readlane(t.upto, 63);
   for (int b0 = 64; b0 < a.c.batch; b0 += 64) t.total += __builtin_amdgcn_readfirstlane(wave_sum(lane_tiles(a, b0 + lane)));
-  t.ranges = kv::ranges_of(t.total, a.target, a.least);
+  t.chunk = kv::chunk_of(t.total, a.target, a.least);
   return t;
 }
 // the sequence that holds tile x and the number of its tiles before x
-__device__ __forceinline__ void find_tile(const Args& a, const Tiles& t, int64_t x, int& b, int& before) {
+__device__ __forceinline__ void find_tile(const Args& a, const Tiles& t, int x, int& b, int& before) {
   const int lane = threadIdx.x & 63;
-  int64_t sum = 0;
+  int sum = 0;
   int mine = t.mine, upto = t.upto;
   for (int b0 = 0;; b0 += 64) {
     if (b0 > 0) {
@@ -81,16 +80,17 @@ __device__ __forceinline__ void find_tile(const Args& a, const Tiles& t, int64_t
     if (hit || b0 + 64 >= a.c.batch) {
       const int at = hit ? __builtin_ctzll(hit) : 63;
       b = __builtin_amdgcn_readfirstlane(b0 + at);
-      before = __builtin_amdgcn_readfirstlane((int)(x - sum) - __shfl(upto - mine, at, 64));
+      before = x - sum - __builtin_amdgcn_readlane(upto - mine, at);
       return;
     }
-    sum += __builtin_amdgcn_readfirstlane(__shfl(upto, 63, 64));
+    sum += __builtin_amdgcn_readlane(upto, 63);
   }
 }
 // tiles of the sequences before b
-__device__ __forceinline__ int64_t tiles_before(const Args& a, int b) {
+__device__ __forceinline__ int tiles_before(const Args& a, const Tiles& t, int b) {
   const int lane = threadIdx.x & 63;
-  int64_t sum = 0;
+  if (b < 64) return __builtin_amdgcn_readlane(t.upto - t.mine, b);
+  int sum = 0;
   for (int b0 = 0; b0 < b; b0 += 64) sum += wave_sum(b0 + lane < b ? lane_tiles(a, b0 + lane) : 0);
   return sum;
 }
@@ -121,17 +121,16 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
   const int col = lane & 15, g = lane >> 4;
   const int kvh = blockIdx.y, room = room_of(a.c), range = blockIdx.x;
   const Tiles plan = count_tiles(a);
-  if (plan.total == 0 || range >= plan.ranges) return;
-  const int64_t begin = kv::range_begin(plan.total, plan.ranges, range);
-  const int64_t end = kv::range_begin(plan.total, plan.ranges, range + 1);
+  const int64_t from = (int64_t)range * plan.chunk;
+  if (from >= plan.total) return;
+  const int begin = (int)from, end = plan.total - begin < plan.chunk ? plan.total : begin + plan.chunk;
   const TileLoads<D, kv::kStep> loads(a.c);
-  const int gp = kv::v_run(1 << a.c.shift);
-  const int v_off = kv::v_at(col, g, gp);
+  const int v_off = kv::v_at(col, g, kv::v_run(a.c.shift));
   int k_off[4];  // K tile j: this lane's row
 #pragma unroll
   for (int j = 0; j < 4; ++j) k_off[j] = 16 * (col >> 2) + 4 * j + (col & 3);
 
-  for (int64_t x0 = begin; x0 < end;) {  // the sequences of the range
+  for (int x0 = begin; x0 < end;) {  // the sequences of the range
   int b, tile0;
   find_tile(a, plan, x0, b, tile0);
   const kv::Rows rows = kv::rows_of(a.cu, b, a.T);
@@ -139,7 +138,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
   len = len < 0 ? 0 : len;
   const kv::Range all = kv::seen_range(len, room, rows.n, 0, rows.n, a.window, a.full);
   const int tiles = kv::tiles_of(all);
-  const int tile1 = end - x0 < tiles - tile0 ? tile0 + (int)(end - x0) : tiles;
+  const int tile1 = end - x0 < tiles - tile0 ? tile0 + (end - x0) : tiles;
   const bool direct = tile0 == 0 && tile1 == tiles;
   const int64_t part = kv::partial_slot(range, x0 == begin);
   x0 += tile1 - tile0;
@@ -150,11 +149,11 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
   const uint32_t buf_lds = lds_offset(buf);
   Pages pages;
   if (count > 0) {
-    pages.load(a.c, b, kvh, first, stride, all.hi);
-    loads.template issue<0, tile_loads(D)>(a.c, pages, 0, first, kvh, buf_lds);
+    pages.load<D>(a.c, b, kvh, first, stride, all.hi);
+    loads.template issue<0, tile_loads(D)>(a.c, pages, 0, buf_lds);
   }
 
-  const Row row = row_at(a, col, kvh, rows.n, len, room);
+  const Row row = row_at(a, col, kvh, rows.n, len, room, true);
   const int any_lo = min16(row.i < 0 ? 0x7FFFFFFF : row.lo), any_hi = max16(row.i < 0 ? 0 : row.hi);
   const int all_lo = max16(row.i < 0 ? 0 : row.lo), all_hi = min16(row.hi);
   Frag<E> q[D / 32];  // column col, elements 64 (s / 2) + 16 g + 8 (s % 2) + 0..7
@@ -173,14 +172,13 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
 
   for (int it = 0; it < count; ++it) {
     const int t0 = first + stride * it, vt = t0 + 16 * g;
-    const int vid = pages.page(it, g);
+    const int vid = pages.gone(it, g);
     const float ks = pages.kscale(it, g) * a.scale2, vs = pages.vscale(it, g);
     const uint8_t* kb = buf + (it & 1) * tile_bytes(D);
     const uint8_t* vb = kb + 64 * D;
     if (it + 1 < count) {
-      if (((it + 1) & 15) == 0) pages.load(a.c, b, kvh, t0 + stride, stride, all.hi);
-      loads.template issue<0, tile_loads(D)>(a.c, pages, it + 1, t0 + stride, kvh,
-                                             buf_lds + ((it + 1) & 1) * tile_bytes(D));
+      if (((it + 1) & 15) == 0) pages.load<D>(a.c, b, kvh, t0 + stride, stride, all.hi);
+      loads.template issue<0, tile_loads(D)>(a.c, pages, it + 1, buf_lds + ((it + 1) & 1) * tile_bytes(D));
       wait_loads<tile_loads(D)>();
     } else {
       wait_loads<0>();
@@ -268,7 +266,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
 #pragma unroll
   for (int jr = threadIdx.x >> 4; jr < 16; jr += kRowsAtOnce) {
     const int jd = threadIdx.x & 15;
-    const Row jrow = row_at(a, jr, kvh, rows.n, len, room);
+    const Row jrow = row_at(a, jr, kvh, rows.n, len, room, true);
     if (jrow.i < 0) continue;
     float M = -INFINITY, L = 0.0f, f[W];
 #pragma unroll
@@ -327,7 +325,7 @@ __global__ __launch_bounds__(256) void attn_join(Args a, int rows_max) {
   if (tiles < 0) return;
   int len = a.c.lens[b];
   len = len < 0 ? 0 : len;
-  const Row row = row_at(a, R, kvh, rows.n, len, room_of(a.c));
+  const Row row = row_at(a, R, kvh, rows.n, len, room_of(a.c), true);
   if (row.i < 0) return;
   const int who = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
   uint16_t* yr = a.y + (int64_t)(rows.first + row.i) * a.yt + (int64_t)row.head * a.yh;
@@ -338,11 +336,11 @@ __global__ __launch_bounds__(256) void attn_join(Args a, int rows_max) {
     return;
   }
   const Tiles plan = count_tiles(a);
-  const int64_t x = tiles_before(a, b);
-  const int r0 = kv::range_of(plan.total, plan.ranges, x), r1 = kv::range_of(plan.total, plan.ranges, x + tiles - 1);
+  const int x = tiles_before(a, plan, b);
+  const int r0 = kv::range_of(plan.chunk, x), r1 = kv::range_of(plan.chunk, x + tiles - 1);
   if (r0 == r1) return;
   const int pieces = r1 - r0 + 1;
-  const bool first_begins = x == kv::range_begin(plan.total, plan.ranges, r0);
+  const bool first_begins = x == r0 * plan.chunk;
   auto at = [&](int i) { return (kv::partial_slot(r0 + i, i > 0 || first_begins) * a.c.heads + kvh) * 16 + R; };
   float M = -INFINITY;
   for (int i = threadIdx.x & 63; i < pieces; i += 64) M = fmaxf(M, a.part_ml[at(i) * 2]);
@@ -442,6 +440,7 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.lse = p.lse;
   a.q_heads = p.q_heads;
   a.group = p.q_heads / p.c.heads;
+  a.group_inverse = (uint32_t)((((uint64_t)1 << 32) + a.group - 1) / a.group);
   a.sign = p.scale < 0.0f ? -1 : (p.scale > 0.0f ? 1 : 0);
   a.scale2 = a.sign == 0 ? 1.0f : (a.sign < 0 ? -p.scale : p.scale) * 1.44269504088896340736f;
   a.window = p.window;

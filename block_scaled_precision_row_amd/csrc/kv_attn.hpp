@@ -19,6 +19,7 @@ struct Args {
   float* lse;
   int64_t qt, qh, yt, yh;
   int q_heads, group;
+  uint32_t group_inverse;  // ceil(2^32 / group), for groups above 1
   float scale2;  // |softmax_scale| * log2(e)
   int64_t window;
   bool full;
@@ -41,9 +42,10 @@ struct Row {
   int head;        // query head
   int lo, hi;      // tokens seen
 };
-__device__ __forceinline__ Row row_at(const Args& a, int R, int kvh, int n, int len, int room) {
+// (`few`: R below 16, divided by a multiplication)
+__device__ __forceinline__ Row row_at(const Args& a, int R, int kvh, int n, int len, int room, bool few = false) {
   Row r;
-  r.i = R / a.group;
+  r.i = !few ? R / a.group : (a.group == 1 ? R : (int)__umulhi((uint32_t)R, a.group_inverse));
   r.head = kvh * a.group + (R - r.i * a.group);
   if (r.i >= n || r.i >= a.max_q_len) {
     r.i = -1;
@@ -113,28 +115,36 @@ __device__ __forceinline__ void wait_loads() {  // until at most n vector-memory
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 
-// The pages of up to 16 tiles of a wave, lane l's granule l % 4 of tile l / 4: page (-1: absent) and scales.
+// The granules of up to 16 tiles of a wave, lane l's granule l % 4 of tile l / 4: whether its page is present, where
+// its codes begin and their scales. An absent page's place is taken by page 0's, whose codes are hidden.
 struct Pages {
-  int id;
+  int absent;  // -1: the page is absent, 0
+  uint32_t k_lo, k_hi, v_lo, v_hi;
   float ks, vs;
-  // tile i starts at token t0 + stride * i; tokens from `end` on are not looked up. Returns whether a page of
-  // those before it is absent.
-  __device__ __forceinline__ bool load(const Cache& c, int b, int head, int t0, int stride, int end) {
+  // tile i starts at token t0 + stride * i; tokens from `end` on are not looked up
+  template <int D>
+  __device__ __forceinline__ void load(const Cache& c, int b, int head, int t0, int stride, int end) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)t0 + (int64_t)stride * (lane >> 2) + 16 * (lane & 3);
-    id = t < end ? kv::page_of(c, b, (int)t) : -1;
-    const int64_t at = (int64_t)(id < 0 ? 0 : id) * c.heads + head;
+    const int id = t < end ? kv::page_of(c, b, (int)t) : -1;
+    absent = id >> 31;
+    const int64_t at = (int64_t)(id < 0 ? 0 : id) * c.heads + head, codes = (at << c.shift) * D;
+    const int in = (int)t & ((1 << c.shift) - 1);
     ks = c.ks[at];
     vs = c.vs[at];
-    return __ballot(t < end && id < 0) != 0;
+    const int64_t k = codes + in * D, v = codes + in;
+    k_lo = (uint32_t)k;
+    k_hi = (uint32_t)(k >> 32);
+    v_lo = (uint32_t)v;
+    v_hi = (uint32_t)(v >> 32);
   }
-  __device__ __forceinline__ int page(int tile, int gran) const { return __shfl(id, (tile & 15) * 4 + gran, 64); }
-  __device__ __forceinline__ float kscale(int tile, int gran) const { return __shfl(ks, (tile & 15) * 4 + gran, 64); }
-  __device__ __forceinline__ float vscale(int tile, int gran) const { return __shfl(vs, (tile & 15) * 4 + gran, 64); }
+  static __device__ __forceinline__ int place(int tile, int gran) { return (tile & 15) * 4 + gran; }
+  __device__ __forceinline__ int gone(int tile, int gran) const { return __shfl(absent, place(tile, gran), 64); }
+  __device__ __forceinline__ float kscale(int tile, int gran) const { return __shfl(ks, place(tile, gran), 64); }
+  __device__ __forceinline__ float vscale(int tile, int gran) const { return __shfl(vs, place(tile, gran), 64); }
 };
 
-// Issues loads [first, last) of the tile at token t0 (its tile number `tile` in `pages`) into LDS at `lds`. An
-// absent page's place is filled from page 0, whose codes are hidden afterwards.
+// Issues loads [first, last) of a tile (its number `tile` in `pages`) into LDS at `lds`.
 template <int D, kv::Kind kind>
 struct TileLoads {
   int k_lane[D / 64];  // granule 0's offsets; another granule exchanges pieces: an exclusive or
@@ -143,28 +153,34 @@ struct TileLoads {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) k_lane[i] = kv::k_source<D, kind>(i, 0, lane);
-    const kv::VSource v = kv::v_source(lane, kv::v_run(1 << c.shift));
+    const kv::VSource v = kv::v_source(lane, kv::v_run(c.shift));
     v_gran = v.gran;
     v_col = v.col;
   }
   template <int first, int last>
-  __device__ __forceinline__ void issue(const Cache& c, const Pages& pages, int tile, int t0, int head,
-                                        uint32_t lds) const {
-    const int ps = 1 << c.shift;
-    const int vid = pages.page(tile, v_gran);
-    const uint8_t* vp = c.v + kv::codes_at(c, vid < 0 ? 0 : vid, head) + (int64_t)v_col * ps +
-                        ((t0 + 16 * v_gran) & (ps - 1));
+  __device__ __forceinline__ void issue(const Cache& c, const Pages& pages, int tile, uint32_t lds) const {
+    if constexpr (first < D / 16) {
 #pragma unroll
-    for (int n = first; n < last; ++n) {
-      if (n < D / 16) {
-        const int gran = n / (D / 64), i = n % (D / 64);
-        const int kid = __builtin_amdgcn_readlane(pages.id, (tile & 15) * 4 + gran);
-        const uint8_t* kp = c.k + kv::codes_at(c, kid < 0 ? 0 : kid, head) +
-                            (int64_t)((t0 + 16 * gran) & (ps - 1)) * D;
-        load_to_lds(kp + (k_lane[i] ^ (16 * kv::k_flip<D, kind>(16 * gran))), lds + 1024 * n);
-      } else {
-        load_to_lds(vp + (int64_t)16 * (n - D / 16) * ps, lds + 1024 * n);
+      for (int gran = first / (D / 64); gran * (D / 64) < last && gran < 4; ++gran) {
+        const int at = Pages::place(tile, gran);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)pages.k_lo, at);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)pages.k_hi, at);
+        const uint8_t* kp = c.k + ((int64_t)hi << 32 | lo);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const int n = gran * (D / 64) + i;
+          if (n >= first && n < last)
+            load_to_lds(kp + (k_lane[i] ^ (16 * kv::k_flip<D, kind>(16 * gran))), lds + 1024 * n);
+        }
       }
+    }
+    if constexpr (last > D / 16) {
+      const int at = Pages::place(tile, v_gran);
+      const uint32_t lo = (uint32_t)__shfl((int)pages.v_lo, at, 64), hi = (uint32_t)__shfl((int)pages.v_hi, at, 64);
+      const uint8_t* vp = c.v + ((int64_t)hi << 32 | lo) + (v_col << c.shift);
+#pragma unroll
+      for (int n = first > D / 16 ? first : D / 16; n < last; ++n)
+        load_to_lds(vp + ((n - D / 16) << (4 + c.shift)), lds + 1024 * n);
     }
   }
 };

@@ -103,16 +103,14 @@ BSQ_HD Range seen_range(int len, int room, int n, int i0, int rows, int64_t wind
 }
 BSQ_HD int tiles_of(Range r) { return (r.hi - r.lo + kTile - 1) / kTile; }
 
-// The tiles of all sequences, one after the other, are cut into `ranges` equal runs, one to a workgroup, which
-// may end one sequence and begin another. So a batch of any raggedness keeps all workgroups equally long,
-// and the host needs to know no length.
-BSQ_HD int ranges_of(int64_t total, int target, int least) {
-  const int64_t r = total / least;
-  return (int)(r < 1 ? 1 : (r > target ? target : r));
+// The tiles of all sequences, one after the other, are cut into equal runs of `chunk` tiles, one to a
+// workgroup, which may end one sequence and begin another. So a batch of any raggedness keeps all workgroups
+// equally long, and the host needs to know no length. (The caller keeps the total below 2^31.)
+BSQ_HD int chunk_of(int total, int target, int least) {
+  const int c = (int)(((unsigned)total + (unsigned)target - 1) / (unsigned)target);
+  return c < least ? least : c;
 }
-BSQ_HD int64_t range_begin(int64_t total, int ranges, int r) { return total * r / ranges; }
-// the range that holds tile x: the last r with total * r / ranges <= x
-BSQ_HD int range_of(int64_t total, int ranges, int64_t x) { return (int)(((x + 1) * ranges - 1) / total); }
+BSQ_HD int range_of(int chunk, int x) { return (int)((unsigned)x / (unsigned)chunk); }
 // A sequence that lies in several ranges leaves a partial result in each: at most one range begins inside
 // it or with it (slot 2 r) for every one but the first, which may hold others before it (slot 2 r + 1).
 BSQ_HD int64_t partial_slot(int r, bool at_begin) { return 2 * (int64_t)r + (at_begin ? 0 : 1); }
@@ -150,20 +148,20 @@ template <int D, Kind kind>
 BSQ_HD int k_at(int token, int piece) {
   return token * D + 16 * (piece ^ k_flip<D, kind>(token));
 }
-// V: granules of an element that lie side by side in a page (at most a tile's four)
-BSQ_HD int v_run(int page) { return page >= 64 ? 4 : page / 16; }
+// V: a page holds 1 << run granules of an element side by side (at most a tile's four)
+BSQ_HD int v_run(int page_shift) { return page_shift >= 6 ? 2 : page_shift - 4; }
 // where the 16 tokens of granule g of element `d` lie in the tile's V
-BSQ_HD int v_at(int d, int g, int gp) {
-  const int c = d & 15;
-  return (d >> 4) * 1024 + 16 * ((g / gp) * (16 * gp) + c * gp + ((g % gp) ^ (c * gp >> 4)));
+BSQ_HD int v_at(int d, int g, int run) {
+  const int c = d & 15, in = (1 << run) - 1;
+  return (d >> 4) * 1024 + 16 * (((g >> run) << (4 + run)) + (c << run) + ((g & in) ^ (c << run >> 4)));
 }
 // granule and element (of 16) that lane `lane` fetches in each of its V loads
 struct VSource {
   int gran, col;
 };
-BSQ_HD VSource v_source(int lane, int gp) {
-  const int run = lane / (16 * gp), rest = lane % (16 * gp), col = rest / gp;
-  return VSource{run * gp + ((rest % gp) ^ (col * gp >> 4)), col};
+BSQ_HD VSource v_source(int lane, int run) {
+  const int in = (1 << run) - 1, col = lane >> run & 15;
+  return VSource{((lane >> (4 + run)) << run) + ((lane & in) ^ (col << run >> 4)), col};
 }
 
 }  // namespace kv

@@ -95,15 +95,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
   const TileLoads<D, kv::kPrompt> loads(a.c);
   constexpr int kMine = tile_loads(D) / 4;  // a wave's share of a tile's loads
   Pages pages;
-  auto issue = [&](int tile, int t0, uint32_t at) __attribute__((always_inline)) {
-    if (wave == 0) loads.template issue<0, kMine>(a.c, pages, tile, t0, kvh, at);
-    else if (wave == 1) loads.template issue<kMine, 2 * kMine>(a.c, pages, tile, t0, kvh, at);
-    else if (wave == 2) loads.template issue<2 * kMine, 3 * kMine>(a.c, pages, tile, t0, kvh, at);
-    else loads.template issue<3 * kMine, 4 * kMine>(a.c, pages, tile, t0, kvh, at);
+  auto issue = [&](int tile, uint32_t at) __attribute__((always_inline)) {
+    if (wave == 0) loads.template issue<0, kMine>(a.c, pages, tile, at);
+    else if (wave == 1) loads.template issue<kMine, 2 * kMine>(a.c, pages, tile, at);
+    else if (wave == 2) loads.template issue<2 * kMine, 3 * kMine>(a.c, pages, tile, at);
+    else loads.template issue<3 * kMine, 4 * kMine>(a.c, pages, tile, at);
   };
   if (count > 0) {
-    pages.load(a.c, blk.b, kvh, first, kv::kTile, blk.range.hi);
-    issue(0, first, lds);
+    pages.load<D>(a.c, blk.b, kvh, first, kv::kTile, blk.range.hi);
+    issue(0, lds);
   }
 
   const int R = blk.r0 + 32 * wave + col;
@@ -117,10 +117,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
                          : signed_query(*reinterpret_cast<const uint4*>(qr + 32 * (s >> 1) + 16 * h + 8 * (s & 1)), a.sign);
   }
   const int k_token = 32 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);  // K tile 0's row; tile 1's is 16 on
-  const int gp = kv::v_run(1 << a.c.shift);
+  const int run = kv::v_run(a.c.shift);
   int v_off[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) v_off[j] = kv::v_at(col, 2 * h + j, gp);
+  for (int j = 0; j < 2; ++j) v_off[j] = kv::v_at(col, 2 * h + j, run);
 
   v16f acc[D / 32];
 #pragma unroll
@@ -183,15 +183,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
   auto advance = [&](int it, int t0, int(&vid)[2], float(&ks)[2], float(&vs)[2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      vid[j] = pages.page(it, 2 * h + j);
+      vid[j] = pages.gone(it, 2 * h + j);
       ks[j] = pages.kscale(it, 2 * h + j) * a.scale2;
       vs[j] = pages.vscale(it, 2 * h + j);
     }
     wait_loads<0>();
     __syncthreads();
     if (it + 1 < count) {
-      if (((it + 1) & 15) == 0) pages.load(a.c, blk.b, kvh, t0 + kv::kTile, kv::kTile, blk.range.hi);
-      issue(it + 1, t0 + kv::kTile, lds + ((it + 1) & 1) * tile_bytes(D));
+      if (((it + 1) & 15) == 0) pages.load<D>(a.c, blk.b, kvh, t0 + kv::kTile, kv::kTile, blk.range.hi);
+      issue(it + 1, lds + ((it + 1) & 1) * tile_bytes(D));
     }
   };
   // Tiles [whole_begin, whole_end), which all rows of the block see whole, run in a loop of their own, the others
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
     for (int it = from; it < to; ++it) {
       const int t0 = first + kv::kTile * it;
       const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
-      const int vgran = pages.page(it, loads.v_gran);
+      const int vgran = pages.gone(it, loads.v_gran);
       int vid[2];
       float ks[2], vs[2];
       advance(it, t0, vid, ks, vs);

@@ -94,17 +94,16 @@ void check_attention(const Cache& c, const std::vector<int32_t>& cu, int64_t T, 
   if (total == 0) return;
   // the ranges as the workgroups walk them: every tile of every sequence once, partial results in slots of
   // their own, and the joining looks for exactly those
-  const int ranges = ranges_of(total, target, least);
-  if (ranges < 1 || ranges > target || range_begin(total, ranges, 0) != 0 || range_begin(total, ranges, ranges) != total)
-    fail("ranges", ranges, target, total, 0);
+  const int chunk = chunk_of((int)total, target, least);
+  const int ranges = range_of(chunk, (int)total - 1) + 1;
+  if (ranges < 1 || ranges > target) fail("ranges", ranges, target, total, chunk);
   std::vector<int64_t> before((size_t)c.batch + 1, 0);
   for (int b = 0; b < c.batch; ++b) before[b + 1] = before[b] + (tiles[b] > 0 ? tiles[b] : 0);
   std::set<int64_t> slots;
   std::vector<std::set<int64_t>> left((size_t)c.batch);
   std::vector<int64_t> done((size_t)c.batch, 0);
   for (int r = 0; r < ranges; ++r) {
-    const int64_t begin = range_begin(total, ranges, r), end = range_begin(total, ranges, r + 1);
-    if (end - begin > (total + ranges - 1) / ranges + 1) fail("range size", r, end - begin, total, ranges);
+    const int64_t begin = (int64_t)r * chunk, end = begin + chunk < total ? begin + chunk : total;
     for (int64_t x = begin; x < end;) {
       int b = 0;
       while (before[b + 1] <= x) ++b;
@@ -116,7 +115,7 @@ void check_attention(const Cache& c, const std::vector<int32_t>& cu, int64_t T, 
         if (s < 0 || s >= 2 * (int64_t)target || !slots.insert(s).second) fail("slot", b, r, s, 0);
         left[b].insert(s);
       }
-      if (range_of(total, ranges, x) != r || range_of(total, ranges, x + (t1 - t0) - 1) != r) fail("range of a tile", b, r, x, 0);
+      if (range_of(chunk, (int)x) != r || range_of(chunk, (int)(x + (t1 - t0) - 1)) != r) fail("range of a tile", b, r, x, 0);
       x += t1 - t0;
       ++g_checked;
     }
@@ -124,10 +123,10 @@ void check_attention(const Cache& c, const std::vector<int32_t>& cu, int64_t T, 
   for (int b = 0; b < c.batch; ++b) {
     if (tiles[b] <= 0) continue;
     if (done[b] != tiles[b]) fail("tiles left out", b, done[b], tiles[b], 0);
-    const int r0 = range_of(total, ranges, before[b]), r1 = range_of(total, ranges, before[b + 1] - 1);
+    const int r0 = range_of(chunk, (int)before[b]), r1 = range_of(chunk, (int)before[b + 1] - 1);
     std::set<int64_t> want;
     if (r0 != r1)
-      for (int r = r0; r <= r1; ++r) want.insert(partial_slot(r, r > r0 || before[b] == range_begin(total, ranges, r0)));
+      for (int r = r0; r <= r1; ++r) want.insert(partial_slot(r, r > r0 || before[b] == (int64_t)r0 * chunk));
     if (want != left[b]) fail("the join looks elsewhere", b, r0, r1, (long)left[b].size());
   }
 }
@@ -175,20 +174,20 @@ void check_k_tile() {
 }
 void check_v_tile() {
   for (int page : {16, 32, 64, 128, 256}) {
-    const int gp = v_run(page);
+    const int run = v_run(__builtin_ctz(page)), gp = 1 << run;
     std::vector<int> seen(64, 0);
     for (int lane = 0; lane < 64; ++lane) {
-      const VSource v = v_source(lane, gp);
+      const VSource v = v_source(lane, run);
       if (v.gran < 0 || v.gran > 3 || v.col < 0 || v.col > 15) fail("V source", page, lane, v.gran, v.col);
       seen[(size_t)(16 * v.gran + v.col)]++;
       for (int blk = 0; blk < 16; ++blk)
-        if (v_at(16 * blk + v.col, v.gran, gp) != 1024 * blk + 16 * lane) fail("V read finds another piece", page, lane, blk, 0);
+        if (v_at(16 * blk + v.col, v.gran, run) != 1024 * blk + 16 * lane) fail("V read finds another piece", page, lane, blk, 0);
     }
     for (int s : seen)
       if (s != 1) fail("V piece not fetched once", page, s, 0, 0);
     for (int g = 0; g < 4; ++g) {
       std::vector<int> at;
-      for (int c = 0; c < 16; ++c) at.push_back(v_at(c, g, gp));
+      for (int c = 0; c < 16; ++c) at.push_back(v_at(c, g, run));
       apart("V bank conflict", at);
     }
     // a tile's granules lie in pages as v_run says

@@ -30,13 +30,13 @@ def test_every_page_and_piece_is_in_bounds(tmp_path):
     ("+ 2 * (int64_t)b;", "+ (int64_t)b;"),                                                   # too few slots
     ("hi = hi < lo ? lo : (hi > t ? t : hi);", "hi = hi < lo ? lo : hi;"),                    # rows past T
     ("if (r.n == 0 || past < 0) return none;", "if (r.n == 0) return none;"),                 # a negative position
-    ("return (int)(((x + 1) * ranges - 1) / total);", "return (int)(x * ranges / total);"),
+    ("(unsigned)total + (unsigned)target - 1) / (unsigned)target", "(unsigned)total) / (unsigned)target"),
     ("2 * (int64_t)r + (at_begin ? 0 : 1)", "(int64_t)r"),
     ("lo = lo / kTile * kTile;", ""),
     ("if (hi > room) hi = room;", ""),
     ("if (D == 64) return gran;", "if (D == 64) return token & 3;"),                          # a bank conflict
     ("return token * D + 16 * (piece ^ k_flip<D, kind>(token));", "return token * D + 16 * piece;"),
-    ("c * gp + ((g % gp) ^ (c * gp >> 4))", "c * gp + g % gp"),
+    ("(c << run) + ((g & in) ^ (c << run >> 4))", "(c << run) + (g & in)"),
 ])
 def test_planted_mistakes_are_found(tmp_path, old, new):
     src = open(os.path.join(CSRC, "kv_index.hpp")).read()
