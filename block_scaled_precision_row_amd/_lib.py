@@ -590,29 +590,41 @@ def bsq_dequant_to_bf16(fmt, w, w_scale, w_scale2=None, out=None):
 _DTYPES = {torch.bfloat16: BSQ_BF16, torch.float16: BSQ_FP16, torch.float32: BSQ_FP32}
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from a build without a GPU
+
+
 def _call(fn, device, *args):
-    """lib.<fn>(*args, current stream) on `device`."""
-    if torch.cuda.current_device() == device.index:
-        _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+    """lib.<fn>(*args, current stream) on `device`. (The handle alone: building a Stream object for it costs 2 us,
+    as much as the launch.)"""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        _check(fn, getattr(lib, fn)(*args, _raw_stream(index)))
         return
     with torch.cuda.device(device):
-        _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+        _check(fn, getattr(lib, fn)(*args, _raw_stream(index)))
 
 
 def _heads(x, dtypes, name):
     """A [tokens, heads, dim] tensor, dim contiguous: (shape, token stride, head stride)."""
     if x.dim() != 3 or x.dtype not in dtypes or not x.is_cuda:
         raise ValueError("%s must be a 3-D tensor of %s on the GPU" % (name, " or ".join(map(str, dtypes))))
-    T, H, D = x.shape
+    shape = x.shape
+    T, H, D = shape
     st, sh, sd = x.stride()
     if sd != 1 and D > 1:
         raise ValueError("%s must have unit stride along its last dimension" % name)
-    return (T, H, D), (st if T > 1 else 0), (sh if H > 1 else 0)
+    return shape, (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
 def _like(x, shape, dtype, device, name):
-    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != device:
+    if x.dtype != dtype or x.shape != shape or x.device != device:
         raise ValueError("%s must be a %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
+
+
+def _heads_like(x, shape, dtype, device, name):
+    """(token stride, head stride) of a [tokens, heads, dim] tensor of this shape."""
+    _like(x, shape, dtype, device, name)
+    return _heads(x, (dtype,), name)[1:]
 
 
 def _flat(x, shape, dtype, device, name):
@@ -635,16 +647,18 @@ def bsq_rope_inv_freq(rot_dim, base, scaling=BSQ_ROPE_PLAIN, factor=1.0, trained
 def bsq_rope(x, positions, inv_freq, layout=BSQ_ROPE_HALF, attn_factor=1.0, backward=False, y=None):
     """x [T, H, D] (bf16, fp16 or fp32) with its first 2 * len(inv_freq) elements rotated to `positions`
     (int64 [T]); backward: the gradient of x for x = the gradient of y. y may be x (in place)."""
-    (T, H, D), xt, xh = _heads(x, _DTYPES, "x")
-    dev = x.device
+    shape, xt, xh = _heads(x, _DTYPES, "x")
+    T, H, D = shape
+    dev, dtype = x.device, x.dtype
     if y is None:
-        y = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-    _like(y, (T, H, D), x.dtype, dev, "y")
-    _, yt, yh = _heads(y, _DTYPES, "y")
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        yt, yh = (H * D if T > 1 else 0), (D if H > 1 else 0)
+    else:
+        yt, yh = _heads_like(y, shape, dtype, dev, "y")
     pos = _flat(positions, (T,), torch.int64, dev, "positions")
     pairs = inv_freq.shape[0]
     freq = _flat(inv_freq, (pairs,), torch.float32, dev, "inv_freq")
-    _call("bsq_rope", dev, _DTYPES[x.dtype], x.data_ptr(), xt, xh, pos, freq, 2 * pairs, layout, attn_factor,
+    _call("bsq_rope", dev, _DTYPES[dtype], x.data_ptr(), xt, xh, pos, freq, 2 * pairs, layout, attn_factor,
           BSQ_ROPE_BACKWARD if backward else 0, y.data_ptr(), yt, yh, T, H, D)
     return y
 
@@ -676,9 +690,9 @@ def bsq_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_s
     [pages, kv_heads, dim, page], k_scale / v_scale fp32 [pages, kv_heads], block_table int32 [B, max_pages]. With
     inv_freq the keys are rotated on the way, and q [T, q_heads, dim] into q_out (may be q), which is returned."""
     dev = k.device
-    (T, H, D), kt, kh = _heads(k, _HALF_TYPES, "k")
-    _like(v, (T, H, D), k.dtype, dev, "v")
-    _, vt, vh = _heads(v, _HALF_TYPES, "v")
+    shape, kt, kh = _heads(k, _HALF_TYPES, "k")
+    T, H, D = shape
+    vt, vh = _heads_like(v, shape, k.dtype, dev, "v")
     c, heads, dim, cu = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, dev)
     if (heads, dim) != (H, D):
         raise ValueError("k has %d heads of %d elements, the cache %d of %d" % (H, D, heads, dim))
@@ -688,12 +702,11 @@ def bsq_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_s
     qp = op = None
     qt = qh = ot = oh = Hq = 0
     if q is not None:
-        (_, Hq, _), qt, qh = _heads(q, _HALF_TYPES, "q")
-        _like(q, (T, Hq, D), k.dtype, dev, "q")
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qt, qh = _heads_like(q, (T, Hq, D), k.dtype, dev, "q")
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        _like(q_out, (T, Hq, D), q.dtype, dev, "q_out")
-        _, ot, oh = _heads(q_out, _HALF_TYPES, "q_out")
+        ot, oh = _heads_like(q_out, (T, Hq, D), q.dtype, dev, "q_out")
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -712,14 +725,16 @@ def bsq_attention_kv8(q, cu_seqlens, seq_lens, block_table, k_cache, v_cache, k_
     cache that bsq_kv_append fills; max_q_len: at least the most rows of a sequence (1 for a decode step).
     softmax_scale: dim ** -0.5 where None. Returns (y [T, q_heads, dim], lse [T, q_heads] fp32)."""
     dev = q.device
-    (T, Hq, D), qt, qh = _heads(q, _HALF_TYPES, "q")
+    shape, qt, qh = _heads(q, _HALF_TYPES, "q")
+    T, Hq, D = shape
     c, H, dim, cu = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, dev)
     if D != dim:
         raise ValueError("q has heads of %d elements, the cache of %d" % (D, dim))
     if y is None:
-        y = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    _like(y, (T, Hq, D), q.dtype, dev, "y")
-    _, yt, yh = _heads(y, _HALF_TYPES, "y")
+        y = torch.empty(shape, dtype=q.dtype, device=dev)
+        yt, yh = (Hq * D if T > 1 else 0), (D if Hq > 1 else 0)
+    else:
+        yt, yh = _heads_like(y, shape, q.dtype, dev, "y")
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     lse_p = _flat(lse, (T, Hq), torch.float32, dev, "lse")

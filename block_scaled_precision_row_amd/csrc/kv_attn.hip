@@ -408,7 +408,7 @@ Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t k
   }
   return p;
 }
-constexpr int kLeastTiles = 4;
+constexpr int kLeastTiles = 2;
 
 template <class E, int D>
 hipError_t launch_step(const Args& a, const Cut& p, hipStream_t s) {
