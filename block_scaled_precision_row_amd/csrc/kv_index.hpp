@@ -38,12 +38,6 @@ BSQ_HD Rows rows_of(const int32_t* cu, int b, int64_t T) {
   return Rows{lo, hi - lo};
 }
 
-// tokens of sequence b that the table has room for
-BSQ_HD int tokens_of(const Cache& c, int b) {
-  const int len = c.lens[b], room = c.max_pages << c.shift;
-  return len < 0 ? 0 : (len > room ? room : len);
-}
-
 // the page of sequence b's token t, -1 where it is absent
 BSQ_HD int page_of(const Cache& c, int b, int t) {
   const int j = t >> c.shift;
@@ -67,7 +61,7 @@ BSQ_HD int64_t first_slot(const int32_t* cu, int b, int64_t T, int shift) {
 }
 BSQ_HD int64_t append_slots(int64_t T, int64_t batch, int shift) { return (T >> shift) + 2 * batch; }
 
-// what slot `first_slot(b) + j` appends: tokens [at, at + n) of page `page`, from row `row` on
+// what slot `first_slot(b) + j` appends: tokens [at, at + n) of page `page` (-1: absent), from row `row` on
 struct Touched {
   int page, at, n, row;
 };
@@ -78,11 +72,9 @@ BSQ_HD Touched touched_page(const Cache& c, const int32_t* cu, int b, int64_t j,
   if (r.n == 0 || past < 0) return none;
   const int64_t start = ((past >> c.shift) + j) << c.shift;
   if (start >= len || (start >> c.shift) >= c.max_pages) return none;
-  const int page = page_of(c, b, (int)start);
-  if (page < 0) return none;
   const int64_t lo = past > start ? past : start;
   const int64_t end = start + ((int64_t)1 << c.shift), hi = len < end ? len : end;
-  return Touched{page, (int)(lo - start), (int)(hi - lo), (int)(r.first + (lo - past))};
+  return Touched{page_of(c, b, (int)start), (int)(lo - start), (int)(hi - lo), (int)(r.first + (lo - past))};
 }
 
 // ---- attention: the tokens of a sequence split over workgroups -----------------------------

@@ -61,10 +61,13 @@ struct Fp32 {
 
 // eight consecutive elements as fp32, 16-byte (16-bit types) or 2 x 16-byte accesses
 template <class T>
-__device__ __forceinline__ void load8(const typename T::elem* p, float (&f)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   f[0] = T::lo(v.x); f[1] = T::hi(v.x); f[2] = T::lo(v.y); f[3] = T::hi(v.y);
   f[4] = T::lo(v.z); f[5] = T::hi(v.z); f[6] = T::lo(v.w); f[7] = T::hi(v.w);
+}
+template <class T>
+__device__ __forceinline__ void load8(const typename T::elem* p, float (&f)[8]) {
+  unpack8<T>(*reinterpret_cast<const uint4*>(p), f);
 }
 template <>
 __device__ __forceinline__ void load8<Fp32>(const float* p, float (&f)[8]) {
