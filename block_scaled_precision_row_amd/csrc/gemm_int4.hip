@@ -1,18 +1,17 @@
 // Few-token linears with 4-bit integer weights and group scales:
 //   y[m][n] = sum_g s[n][g] * sum_{k in g} x[m][k] (c[n][k] - z[n][g]).
 //
-// 16 weight rows a workgroup, its waves taking every fourth stage of 128 K values; the products of
-// 16 tokens run on 16x16x32 MFMA (A: x, B: W), 32 K values an instruction, so that a group's sum
-// is complete in the accumulator before its scale is applied in fp32. A lane loads 16 bytes of a
-// row (32 K values: whole 64-byte segments a row and stage); a 4 x 4 exchange of dwords between
-// the four lanes of a row (four lane-swap instructions) then gives every lane eight values of each
-// block of 32. Codes become 16-bit numbers by or-ing them into the mantissa of a power of two:
+// Codes become 16-bit numbers by or-ing them into the mantissa of a power of two:
 //   fp16: 1024 + c, from which a packed subtraction of 1024 + z leaves c - z exactly;
-//   bf16 (no packed arithmetic): 128 + c stays, and the sum of x over the group, from one more
-//   MFMA against ones, takes (128 + z) sum x away in fp32.
-// The order of nibbles in a dword gives pairs (k, k + 4); x is put in the same order.
+//   bf16 (no packed arithmetic): 128 + c stays, and (128 + z) times the sum of x over the group is taken away in
+//   fp32.
+// The order of nibbles in a dword gives pairs (k, k + 4); x is put in the same order. A group's sum is complete in
+// fp32 before its scale is applied.
 //
-// Bound by memory: K / 2 bytes a row and its scales.
+// The floor is memory: K / 2 bytes a row and its scales (cold: 1 x 16384 x 8192 18.9 us, 3.9 TB/s; 1 x 4096 x 4096
+// 5.2 us, of which a launch is 3). With more tokens vector instructions bound it, some twelve for eight codes and
+// as many for each 8 x 16 values of x (24 x 12288 x 4096 in groups of 32: 26.3 us, the vector units 40 % busy, as
+// far as two waves a SIMD take them).
 #include <type_traits>
 
 #include "bsq_launch.hpp"
@@ -45,10 +44,14 @@ union Frag {
 // the eight values of a dword as pairs (k, k + 4)
 template <class E>
 __device__ __forceinline__ typename E::vec8 codes8(uint32_t w, uint32_t minus) {
-  constexpr uint32_t kMagic = E::is_half ? 0x64006400u : 0x43004300u;
+  // (the constants from registers, so that mask and magic number are one instruction: a three-operand one takes no
+  // literal)
+  uint32_t mask = 0x000F000Fu, magic = E::is_half ? 0x64006400u : 0x43004300u;
+  asm("" : "+s"(mask));
+  asm("" : "+v"(magic));
   Frag<E> f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f.u[i] = ((w >> (4 * i)) & 0x000F000Fu) | kMagic;
+  for (int i = 0; i < 4; ++i) f.u[i] = ((w >> (4 * i)) & mask) | magic;
   if constexpr (E::is_half) {
     union { uint32_t u; v2h h; } c;
     c.u = minus;
@@ -72,6 +75,11 @@ __device__ __forceinline__ typename E::vec8 paired(uint4 x) {
   return f.v;
 }
 
+// ---- three tokens and more: 16-row tiles on the matrix units ------------------------------
+// A workgroup takes RT tiles of 16 rows, each of its eight waves every eighth stage of 128 K values on 16x16x32 MFMA
+// (A: x, B: W), joined through LDS in order at the end. (A stage of x shared by two or four waves, with the codes
+// four stages ahead: 5 x 16384 x 8192 40 us against 28, for x is then reordered per row tile.)
+//
 // What a wave reads of one stage, as it loads it: whole segments of rows by neighbouring lanes (the four lanes
 // 4 i .. 4 i + 3 read row i's 64 bytes of codes, 16 lanes a token's 256 bytes of x). With the operands' own order
 // (neighbouring lanes on neighbouring rows) the address unit took 49 cycles an instruction and bounded
@@ -266,7 +274,7 @@ __global__ __launch_bounds__(64 * WAVES) void int4_mfma(Args a) {
   }
 }
 
-// ---- up to four tokens: dot products, lanes along K ------------------------------------
+// ---- one token or two: dot products, lanes along K ------------------------------------
 // A lane keeps the 32 x values of its place in a slab of 2048 (16 registers a token) and meets them with
 // its 16 bytes of each row: a wave's load of a row is 1 KB without a gap, a lane's values lie in one
 // group, so its sum is scaled in its own registers. A wave walks blocks of kRows rows, the next
@@ -440,11 +448,11 @@ hipError_t launch_rows(const Args& a, int group, hipStream_t s) {
 }
 template <class E>
 hipError_t launch_tokens(const Args& a, int group, hipStream_t s) {
-  if (a.M <= 4) {
-    if (a.M == 1) return launch_dot<E, 1>(a, group, s);
-    if (a.M == 2) return launch_dot<E, 2>(a, group, s);
-    return launch_dot<E, 4>(a, group, s);
-  }
+  // Dot products up to two tokens, the matrix units above (bf16, dot against matrix units: 16384 x 8192 groups of 64,
+  // 1 token 18.9 and 27.2 us, 2: 23.7 and 27.4, 3: 30.2 and 26.8; 12288 x 4096 groups of 32, 2: 11.3 and 18.3, 3:
+  // 15.9 and 18.5; 4096 x 4096 groups of 128, 2: 6.5 and 7.0, 3: 8.0 and 7.0).
+  if (a.M == 1) return launch_dot<E, 1>(a, group, s);
+  if (a.M == 2) return launch_dot<E, 2>(a, group, s);
   if (a.M <= 16) return launch_rows<E, 1>(a, group, s);
   if (a.M <= 32) return launch_rows<E, 2>(a, group, s);
   return launch_rows<E, 4>(a, group, s);
