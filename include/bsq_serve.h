@@ -98,7 +98,7 @@ bsq_status bsq_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t 
  * cu_seqlens[b + 1] - 1 of a [T] tensor (int32 [batch + 1] device, starting at
  * 0 and not decreasing), and they are its last ones: row cu_seqlens[b] + i has
  * position seq_lens[b] - n_b + i, n_b = cu_seqlens[b + 1] - cu_seqlens[b]. Rows
- * from cu_seqlens[batch] on belong to no sequence: neither read nor written.
+ * from cu_seqlens[batch] on belong to no sequence: not written, and without effect.
  */
 typedef struct {
   uint8_t* k;
