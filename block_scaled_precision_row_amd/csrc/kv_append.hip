@@ -6,11 +6,13 @@
 // exact except for codes that fall below E4M3's normal range, so a page filled token by token
 // holds what it would hold if filled at once, up to those.
 //
+// Keys are rotated in 64 bits, so that next to a border between codes they fall on the right side.
+//
 // Bound by memory for prompts (2 bytes read and 1 written per element, the queries twice 2): 9000 tokens of 32 + 2 x 8
-// heads of 128 in pages of 16, 214 MB, in 51 us, 4.2 TB/s; and by the chain of dependent loads (row, length, page,
-// scale, values) for a decode step: 96 tokens in 9.6 us. What that took for the prompt, from 62 us: one wave to a
-// token's queries with its loads on their way before the search for its sequence (-9), and few enough registers for
-// a sixth wave to a SIMD (-3; capping them instead, which spills ten to the stack, +8).
+// heads of 128 in pages of 16, 214 MB, in 56 us, 3.8 TB/s (50 with angles and products in 32 bits, which
+// put three times as many keys on the wrong side); and by the chain of dependent loads (row, length, page, scale,
+// values) for a decode step: 96 tokens in 10.7 us. What counted for the prompt: one wave to a token's queries with its
+// loads on their way before the search for its sequence (-9 us), and the registers of a thread.
 #include "serve_device.hpp"
 
 namespace bsq {
@@ -66,17 +68,15 @@ __device__ __forceinline__ bool unit_places(int u, int rot, int& e0, int& e1) {
   e1 = e0 + ((turned ? rot : D - rot) >> 1);
   return turned;
 }
-// rotates a unit: its pairs are one element of either piece (at pair e0 + j), or neighbours in a piece
-template <bool INTER, class Angle>
-__device__ __forceinline__ void turn(float (&p)[8], float (&q)[8], int e0, int e1, Angle angle) {
+// rotates a unit by `rotate(pair, x0, x1)`: its pairs are one element of either piece (at pair e0 + j), or neighbours
+// in a piece
+template <bool INTER, class Rotate>
+__device__ __forceinline__ void turn(float (&p)[8], float (&q)[8], int e0, int e1, Rotate rotate) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float2 v = angle(!INTER ? e0 + j : (j < 4 ? (e0 >> 1) + j : (e1 >> 1) + j - 4));
     float& a = INTER ? (j < 4 ? p[(2 * j) & 7] : q[(2 * j) & 7]) : p[j];
     float& b = INTER ? (j < 4 ? p[(2 * j + 1) & 7] : q[(2 * j + 1) & 7]) : q[j];
-    const float a0 = a, b0 = b;
-    a = a0 * v.x - b0 * v.y;
-    b = b0 * v.x + a0 * v.y;
+    rotate(!INTER ? e0 + j : (j < 4 ? (e0 >> 1) + j : (e1 >> 1) + j - 4), a, b);
   }
 }
 
@@ -144,7 +144,14 @@ __device__ __forceinline__ void append_page(const Args& a, int64_t slot, int hea
     load8<E>(kr + (int64_t)t * a.kt + e0, p);
     load8<E>(kr + (int64_t)t * a.kt + e1, q);
     if (turned)
-      turn<INTER>(p, q, e0, e1, [&](int i) { return rope_angle((double)(pos0 + t), a.inv_freq[i], a.factor); });
+      turn<INTER>(p, q, e0, e1, [&](int i, float& x0, float& x1) {
+        // in 64 bits: among millions of keys some lie next to a border between codes, and a value off by
+        // 2^-22 falls on its wrong side three times as often as correctly rounded products do
+        const Turn v = rope_turn((double)(pos0 + t), a.inv_freq[i], a.factor);
+        const double u0 = (double)x0, u1 = (double)x1;
+        x0 = to_odd(fma(u0, v.c, -(u1 * v.s)));
+        x1 = to_odd(fma(u1, v.c, u0 * v.s));
+      });
   };
   float kmax = 0.0f, vmax = 0.0f;
   float keep[KEEP][2][8];
@@ -322,7 +329,13 @@ __device__ __forceinline__ void turn_queries(const Args& a, int64_t t) {
     float p[8], q[8];
     unpack8<E>(v0, p);
     unpack8<E>(v1, q);
-    if (turned) turn<INTER>(p, q, e0, e1, [&](int j) { return cs[j]; });
+    if (turned)
+      turn<INTER>(p, q, e0, e1, [&](int i, float& x0, float& x1) {
+        const float2 v = cs[i];
+        const float u0 = x0, u1 = x1;
+        x0 = u0 * v.x - u1 * v.y;
+        x1 = u1 * v.x + u0 * v.y;
+      });
     uint16_t* dst = orow + (int64_t)h * a.oh;
     store8<E>(dst + e0, p);
     store8<E>(dst + e1, q);

@@ -85,15 +85,47 @@ __device__ __forceinline__ void store8<Fp32>(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// cos and sin of position * w, times `factor`. The product is formed in 64 bits and reduced to a
-// fraction of a turn there (a position of 10^6 keeps 10^-10 of a turn); the remaining angle,
-// below half a turn, is rounded to fp32, an error of at most 2^-25 pi.
+// Cos and sin of position * w, times `factor`, in 64 bits (whose vector instructions take as long as those of 32
+// here): the angle as a fraction of a turn (a position of 10^6 keeps 10^-10 of one), less whole quarters, and the
+// Taylor series on what is left, at most pi / 4: the first terms left out are x^15 / 15! and x^14 / 14!, below 4e-13.
+struct Turn {
+  double c, s;
+};
+__device__ __forceinline__ Turn rope_turn(double position, float w, float factor) {
+  double t = position * (double)w * 0.15915494309189533577;
+  t -= rint(t);
+  const double quarter = rint(4.0 * t);
+  const double x = fma(quarter, -0.25, t) * 6.283185307179586476925, z = x * x;
+  double s = fma(z, 1.0 / 6227020800.0, -1.0 / 39916800.0), c = fma(z, 1.0 / 479001600.0, -1.0 / 3628800.0);
+  s = fma(z, s, 1.0 / 362880.0);
+  c = fma(z, c, 1.0 / 40320.0);
+  s = fma(z, s, -1.0 / 5040.0);
+  c = fma(z, c, -1.0 / 720.0);
+  s = fma(z, s, 1.0 / 120.0);
+  c = fma(z, c, 1.0 / 24.0);
+  s = fma(z, s, -1.0 / 6.0);
+  c = fma(z, c, -0.5);
+  s = fma(x * z, s, x);
+  c = fma(z, c, 1.0);
+  const int q = (int)quarter & 3;
+  double a = q & 1 ? s : c, b = q & 1 ? c : s;
+  a = q == 1 || q == 2 ? -a : a;
+  b = q >= 2 ? -b : b;
+  return Turn{a * (double)factor, b * (double)factor};
+}
 __device__ __forceinline__ float2 rope_angle(double position, float w, float factor) {
-  double turns = position * (double)w * 0.15915494309189533577;
-  turns -= rint(turns);
-  float s, c;
-  sincospif((float)(2.0 * turns), &s, &c);
-  return make_float2(c * factor, s * factor);
+  const Turn t = rope_turn(position, w, factor);
+  return make_float2((float)t.c, (float)t.s);
+}
+
+// x in fp32 with the last bit set where that is not exact: a later rounding to fewer bits (after a power of two)
+// then falls as it would from x itself
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = (float)x;
+  const double back = (double)f;
+  uint32_t u = __float_as_uint(f);
+  if (back != x) u = (fabs(back) > fabs(x) ? u - 1 : u) | 1u;
+  return __uint_as_float(u);
 }
 
 }  // namespace bsq

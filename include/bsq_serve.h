@@ -116,7 +116,7 @@ typedef struct {
  * way (and, on request, the queries too, into q_out). For each page and kv
  * head that receives tokens, for K and V each:
  *   a = the largest finite magnitude among the new values of the page (keys
- *     after the rotation, in fp32), e = the least exponent with a <= 448 * 2^e
+ *     after the rotation, which for keys is done in 64 bits), e = the least exponent with a <= 448 * 2^e
  *     (2^e >= 2^-126; a = 0 counts as scale 0),
  *   scale = max(2^e, the scale before if the page already holds tokens of the
  *     sequence), so that a first token starts its page anew,

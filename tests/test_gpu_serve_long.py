@@ -134,6 +134,25 @@ def test_rows_past_the_promised_length(rows, most):
         assert torch.all((y[e:cu[b + 1]] == 7.0)) and torch.all(lse[e:cu[b + 1]] == 7.0)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_append_rotated_keys_bit_for_bit(kind, interleaved):
+    """Half a million rotated keys: every code is that of the key in 64 bits (angles err by some 2^-45 there, so a key
+    within that of a border between codes, 2^-4 apart, is not among them)."""
+    T, past, H, D = 2000, 37, 2, 128
+    c, cu = Cache(21, [past + T], H, D, 64), starts([T])
+    k, v = (queries(22 + i, T, H, D, kind) for i in range(2))
+    w = L.bsq_rope_inv_freq(D, 500000.0)[0]
+    kc, vc, ks, vs = c.kc.copy(), c.vc.copy(), c.ks.copy(), c.vs.copy()
+    kr = serve.rope(f64(k), np.arange(past, past + T), f64(w), interleaved, 1.25)
+    serve.append(kr, f64(v), cu, c.lens, c.table, kc, vc, ks, vs)
+    lens, table, gk, gv, gks, gvs = c.device()
+    L.bsq_kv_append(k.cuda(), v.cuda(), gpu(cu), lens, table, gk, gv, gks, gvs, w.cuda(),
+                    L.BSQ_ROPE_INTERLEAVED if interleaved else L.BSQ_ROPE_HALF, 1.25)
+    assert np.array_equal(f64(gks), ks) and np.array_equal(f64(gvs), vs)
+    assert np.array_equal(gk.cpu().numpy(), kc) and np.array_equal(gv.cpu().numpy(), vc)
+
+
 def test_append_many_query_heads_in_place():
     """More query elements than a wave keeps ahead, written over the queries."""
     rows = [3, 1]
