@@ -178,6 +178,7 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
     const uint8_t* vb = kb + 64 * D;
     if (it + 1 < count) {
       if (((it + 1) & 15) == 0) pages.load<D>(a.c, b, kvh, t0 + stride, stride, all.hi);
+      wait_reads();
       loads.template issue<0, tile_loads(D)>(a.c, pages, it + 1, buf_lds + ((it + 1) & 1) * tile_bytes(D));
       wait_loads<tile_loads(D)>();
     } else {

@@ -118,6 +118,9 @@ __device__ __forceinline__ void wait_loads() {  // until at most n vector-memory
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 
+// until the wave's own LDS reads have returned (before loads that write where it has read)
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // The granules of up to 16 tiles of a wave, lane l's granule l % 4 of tile l / 4: whether its page is present, where
 // its codes begin and their scales. An absent page's place is taken by page 0's, whose codes are hidden.
 struct Pages {
@@ -133,8 +136,11 @@ struct Pages {
     absent = id >> 31;
     const int64_t at = (int64_t)(id < 0 ? 0 : id) * c.heads + head, codes = (at << c.shift) * D;
     const int in = (int)t & ((1 << c.shift) - 1);
+    // (a scale that is not finite is not append's, but what an unused page happens to hold: its codes are hidden, as 0,
+    // and must not meet it)
     ks = c.ks[at];
     vs = c.vs[at];
+    vs = fabsf(vs) <= 3.40282347e38f ? vs : 0.0f;
     const int64_t k = codes + in * D, v = codes + in;
     k_lo = (uint32_t)k;
     k_hi = (uint32_t)(k >> 32);

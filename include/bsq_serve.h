@@ -90,9 +90,14 @@ bsq_status bsq_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t 
  *   seq_lens [batch] int32: tokens of each sequence, those of the current
  *     call's queries / new tokens included
  * The struct is host memory, read during the call only. head_dim 64, 128 or
- * 256; page_size 16, 32, 64, 128 or 256; kv_heads >= 1, num_pages >= 1 (<
- * 2^31), 0 <= batch <= 65536, max_pages >= 1, table_stride >= max_pages,
- * max_pages * page_size < 2^31 - 1024. k and v 16-byte aligned, the others 4-byte.
+ * 256; page_size 16, 32, 64, 128 or 256; 1 <= kv_heads <= 1024, num_pages >= 1
+ * (< 2^31), 0 <= batch <= 65536, max_pages >= 1, table_stride >= max_pages
+ * (< 2^40), max_pages * page_size < 2^31 - 1024. k and v 16-byte aligned, the
+ * others 4-byte. 0 <= T <= 2^30 and at most 65535 query heads; a call whose
+ * work does not fit one launch is refused (BSQ_ERR_SHAPE): append from
+ * (T / page_size + 2 batch) * kv_heads + T = 2^23 on, attention from
+ * (T * q_heads / kv_heads / 128 + batch) * kv_heads = 2^23 or
+ * batch * (max_pages * page_size / 64 + 1) = 2^31 on.
  *
  * The tokens of a call are packed: sequence b's are rows cu_seqlens[b] to
  * cu_seqlens[b + 1] - 1 of a [T] tensor (int32 [batch + 1] device, starting at
@@ -134,7 +139,7 @@ typedef struct {
  *     nothing is rotated and q_out is a copy.
  * A sequence with seq_lens[b] < n_b is skipped, and so are tokens whose page is
  * absent or lies past max_pages. A page that receives tokens must be in one
- * sequence's table only (two sequences writing one page race: its codes and
+ * sequence's table only, and once (two writers of one page race: its codes and
  * scales are then either's).
  */
 bsq_status bsq_kv_append(bsq_dtype dtype, const bsq_kv8_cache* cache, const int32_t* cu_seqlens, int64_t T,
@@ -164,7 +169,8 @@ bsq_status bsq_kv_append(bsq_dtype dtype, const bsq_kv8_cache* cache, const int3
  *     or a softmax_scale that is not finite
  * A sequence with seq_lens[b] < n_b has negative positions: those rows see
  * nothing (with BSQ_ATTN_FULL they see all). Tokens past max_pages count as
- * absent. Scales have to be what bsq_kv_append writes, powers of two or 0.
+ * absent. The scales of pages that a row sees have to be what bsq_kv_append
+ * writes, powers of two or 0; those of other pages may be anything.
  * Workspace: bsq_attention_kv8_workspace_bytes(...) bytes, 256-byte aligned, not
  * shared by calls that may overlap: partial results of sequences that are
  * split over workgroups; nothing in it needs clearing or survives the call.
@@ -188,8 +194,10 @@ bsq_status bsq_attention_kv8(bsq_dtype dtype, const bsq_kv8_cache* cache, const 
  *   x [M][ldx], y [M][ldy] of `dtype` (BSQ_BF16 or BSQ_FP16)
  *   w [N][K/2], element 2j in the low nibble of byte j
  *   w_scale [N][K/group] of `dtype`; w_zero [N][K/group] uint8 (0..255) or NULL
- * group 32, 64 or 128, K % group == 0; shape, ld and alignment rules of bsq.h
- * (w_scale 2-byte, w_zero 1-byte aligned).
+ * group 32, 64 or 128, K % group == 0; M <= 2^20 - 16, N < 2^27, K <= 2^20; shape,
+ * ld and alignment rules of bsq.h (w_scale 2-byte, w_zero 1-byte aligned). Sums
+ * are of x c (BSQ_BF16: of x (c + 128), which x (z + 128) is taken from), so
+ * they must not leave fp32's range: with |x| below 2^90 none does.
  */
 bsq_status bsq_gemm_int4g(bsq_dtype dtype, const void* x, int64_t ldx, const uint8_t* w, const void* w_scale,
                           const uint8_t* w_zero, int64_t group, void* y, int64_t ldy, int64_t M, int64_t N,

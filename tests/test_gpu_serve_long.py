@@ -84,6 +84,30 @@ def test_long_hidden_nan(rows):
     check(c, cu, q, got[0], got[1], 0.1, 1800)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,window", [([1, 1], 0), ([45, 20], 0), ([1, 1], 90), ([45, 20], 90)])
+def test_scales_of_pages_that_nobody_sees(rows, window, kind):
+    """Pools come uninitialised: scales of pages without tokens, of page 0 among them, and of those in front of the window
+    may be anything."""
+    lens = [230, 75]
+    c, cu, q = Cache(17, lens, 2, 64, 16), starts(rows), queries(18, sum(rows), 4, 64, kind)
+    free = next(p for p in range(c.pages) if p not in c.table)
+    for a in (c.kc, c.vc, c.ks, c.vs):
+        a[[0, free]] = a[[free, 0]]
+    at = np.where(c.table == 0, free, np.where(c.table == free, 0, c.table))
+    c.table = at.astype(np.int32)
+    want = attention(c, cu, q, max(rows), softmax_scale=0.2, window=window)
+    check(c, cu, q, *want, 0.2, window)
+    seen = [c.table[b, t // 16] for b in range(2) for t in range(lens[b])
+            if not window or t > lens[b] - rows[b] - window]
+    hidden = np.setdiff1d(np.arange(c.pages), seen)
+    assert 0 in hidden and (not window or len(hidden) > 2)
+    for bad in (float("nan"), float("inf"), -3e38):
+        c.ks[hidden] = c.vs[hidden] = bad
+        got = attention(c, cu, q, max(rows), softmax_scale=0.2, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("D,H,lens", [(64, 128, [6000, 1, 7100, 5300]), (128, 128, [2300, 4400, 2100]), (256, 64, [3100, 3100, 64, 3700])])
 def test_steps_of_many_tiles_a_wave(D, H, lens):
     """So many kv heads that a workgroup takes whole contexts. All heads hold the same codes and queries: the first
