@@ -23,26 +23,25 @@ namespace {
 
 using namespace attn;
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+// v and what DPP control `ctrl` brings from other lanes of its row or of the rows before (0 where there is none)
+template <int ctrl, int rows>
+__device__ __forceinline__ int add_from(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xF, false);
 }
 __device__ __forceinline__ int wave_scan(int v) {  // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(v, off, 64);
-    if (lane >= off) v += o;
-  }
-  return v;
+  v = add_from<0x111, 0xF>(v);  // within 16 lanes: row_shr 1, 2, 4, 8
+  v = add_from<0x112, 0xF>(v);
+  v = add_from<0x114, 0xF>(v);
+  v = add_from<0x118, 0xF>(v);
+  v = add_from<0x142, 0xA>(v);  // row_bcast 15: rows 0 and 2 to 1 and 3
+  return add_from<0x143, 0xC>(v);  // row_bcast 31: the first half to the second
 }
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
 
 // tiles of sequence b over all its rows; -1 for one that the step kernel does not take
 __device__ __forceinline__ int sequence_tiles(const Args& a, int b) {
-  const int n = kv::rows_of(a.cu, b, a.T).n;
+  const int n = kv::rows_of(a.cu, b, a.T).n, len = a.c.lens[b];  // (loaded together)
   if (n == 0 || (int64_t)n * a.group > a.small) return -1;
-  const int len = a.c.lens[b];
   return kv::tiles_of(kv::seen_range(len < 0 ? 0 : len, room_of(a.c), n, 0, n, a.window, a.full));
 }
 
@@ -62,7 +61,7 @@ __device__ __forceinline__ Tiles count_tiles(const Args& a) {
   t.mine = lane_tiles(a, lane);
   t.upto = wave_scan(t.mine);
   t.total = __builtin_amdgcn_readlane(t.upto, 63);
-  for (int b0 = 64; b0 < a.c.batch; b0 += 64) t.total += __builtin_amdgcn_readfirstlane(wave_sum(lane_tiles(a, b0 + lane)));
+  for (int b0 = 64; b0 < a.c.batch; b0 += 64) t.total += wave_sum(lane_tiles(a, b0 + lane));
   t.chunk = kv::chunk_of(t.total, a.target, a.least);
   return t;
 }
@@ -343,21 +342,36 @@ __global__ __launch_bounds__(256) void attn_join(Args a, int rows_max) {
   const int pieces = r1 - r0 + 1;
   const bool first_begins = x == r0 * plan.chunk;
   auto at = [&](int i) { return (kv::partial_slot(r0 + i, i > 0 || first_begins) * a.c.heads + kvh) * 16 + R; };
+  // this thread's first pieces are on their way while the maximum is found
+  constexpr int kAhead = 4;
+  float4 v[kAhead];
+  float2 ml[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int64_t p = at(who + PER * j < pieces ? who + PER * j : 0);
+    v[j] = *reinterpret_cast<const float4*>(a.part_o + p * D + d);
+    ml[j] = *reinterpret_cast<const float2*>(a.part_ml + p * 2);
+  }
   float M = -INFINITY;
   for (int i = threadIdx.x & 63; i < pieces; i += 64) M = fmaxf(M, a.part_ml[at(i) * 2]);
   M = wave_max(M);
   const float base = finite_base(M);
   float o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, L = 0.0f;
+  auto add = [&](float4 x, float2 r) {
+    const float f = __builtin_amdgcn_exp2f(r.x - base);
+    L += f * r.y;
+    o[0] += f * x.x;
+    o[1] += f * x.y;
+    o[2] += f * x.z;
+    o[3] += f * x.w;
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (who + PER * j < pieces) add(v[j], ml[j]);
 #pragma unroll 4
-  for (int i = who; i < pieces; i += PER) {
+  for (int i = who + PER * kAhead; i < pieces; i += PER) {
     const int64_t p = at(i);
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[p * 2] - base);
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + p * D + d);
-    L += f * a.part_ml[p * 2 + 1];
-    o[0] += f * v.x;
-    o[1] += f * v.y;
-    o[2] += f * v.z;
-    o[3] += f * v.w;
+    add(*reinterpret_cast<const float4*>(a.part_o + p * D + d), *reinterpret_cast<const float2*>(a.part_ml + p * 2));
   }
   *reinterpret_cast<float4*>(&sh[who][d]) = make_float4(o[0], o[1], o[2], o[3]);
   if (d == 0) sh_l[who] = L;

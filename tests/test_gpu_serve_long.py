@@ -299,3 +299,62 @@ def test_every_operator_on_a_stream_of_its_own():
         got = run(dev, late)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_broadcast_operands_and_no_lse():
+    """Queries, keys and values with strides of 0 are what their copies are; lse may be left out."""
+    c = Cache(31, [20, 33], 2, 64, 16)
+    cu, dev = gpu(starts([3, 2])), c.device()
+    one = queries(32, 1, 1, 64, "bf16").cuda()
+    wide, shared = one.expand(5, 4, 64), queries(33, 5, 1, 64, "bf16").cuda().expand(5, 2, 64)
+    w = L.bsq_rope_inv_freq(64, 10000.0)[0].cuda()
+    other = [t.clone() for t in dev]
+    q1 = L.bsq_kv_append(shared, shared, cu, *dev, inv_freq=w, q=wide)
+    q2 = L.bsq_kv_append(shared.contiguous(), shared.contiguous(), cu, *other, inv_freq=w, q=wide.contiguous())
+    assert torch.equal(q1, q2) and all(torch.equal(a, b) for a, b in zip(dev, other))
+    y, lse = L.bsq_attention_kv8(wide, cu, *dev, 3)
+    y2, lse2 = L.bsq_attention_kv8(wide.contiguous(), cu, *dev, 3)
+    assert torch.equal(y, y2) and torch.equal(lse, lse2)
+    s = L.Kv8Cache(*(dev[i].data_ptr() for i in (2, 3, 4, 5, 1, 0)), c.pages, 2, 16, 64, 2, dev[1].shape[1], dev[1].shape[1])
+    n = L.bsq_attention_kv8_workspace_bytes(2, 5, 3, 4, 2, 64)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+    y3 = torch.empty_like(y)
+    args = (L.BSQ_BF16, s, cu.data_ptr(), 5, 3, wide.data_ptr(), 0, 0, 4, 0.125, 0, 0, y3.data_ptr(), 256, 64, None)
+    assert L.lib.bsq_attention_kv8(*args, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_millions_of_tokens_and_negative_positions(interleaved):
+    """More tokens than a dimension of a grid holds, and positions on both sides of 0."""
+    T, D = (1 << 23) + 5, 16
+    x = torch.randn(T, 1, D, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(T, device="cuda") - (1 << 22)
+    w = L.bsq_rope_inv_freq(D, 10000.0)[0].cuda()
+    layout = L.BSQ_ROPE_INTERLEAVED if interleaved else L.BSQ_ROPE_HALF
+    y = L.bsq_rope(x, pos, w, layout)
+    for at in (0, (1 << 22) - 50, T - 200):
+        part = slice(at, at + 200)
+        assert torch.equal(y[part], L.bsq_rope(x[part], pos[part], w, layout))
+        ref = serve.rope(f64(x[part]), pos[part].cpu().numpy(), f64(w), interleaved)
+        a = np.abs(f64(x[part]))
+        pair = a[..., 0::2] + a[..., 1::2] if interleaved else a[..., :8] + a[..., 8:]
+        size = np.repeat(pair, 2, -1) if interleaved else np.concatenate([pair, pair], -1)
+        assert np.all(np.abs(f64(y[part]) - ref) <= u(torch.bfloat16) * np.abs(ref) + 2.0 ** -21 * size)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("M", [1, 2, 3, 33])
+def test_int4_the_longest_rows(M, kind):
+    """K = 2^20."""
+    N, K, group = 5, 1 << 20, 128
+    rng = np.random.default_rng(M)
+    dt = DTYPES[kind]
+    x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).to(dt)
+    w = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    s = torch.from_numpy(rng.uniform(0.0001, 0.001, (N, K // group))).to(dt)
+    ref, size = serve.int4g(f64(x), w, f64(s), None, group)
+    y = f64(L.bsq_gemm_int4g(x.cuda(), gpu(w), s.cuda()))
+    # sums over a group, over a wave's groups and over the waves: (group + K / group + 4) roundings at most
+    bound = u(dt) * np.abs(ref) + (group + K // group + 4) * 2.0 ** -24 * (40.0 if kind == "bf16" else 1.0) * size + 2.0 ** -25
+    assert np.all(np.abs(y - ref) <= bound)
