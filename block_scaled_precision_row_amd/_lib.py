@@ -617,18 +617,24 @@ def _heads(x, dtypes, name):
 
 
 def _like(x, shape, dtype, device, name):
-    if x.dtype != dtype or x.shape != shape or x.device != device:
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device.index:
         raise ValueError("%s must be a %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
 
 
 def _heads_like(x, shape, dtype, device, name):
     """(token stride, head stride) of a [tokens, heads, dim] tensor of this shape."""
-    _like(x, shape, dtype, device, name)
-    return _heads(x, (dtype,), name)[1:]
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device.index:
+        _like(x, shape, dtype, device, name)
+    T, H, D = shape
+    st, sh, sd = x.stride()
+    if sd != 1 and D > 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
 def _flat(x, shape, dtype, device, name):
-    _like(x, shape, dtype, device, name)
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device.index:
+        _like(x, shape, dtype, device, name)
     if not x.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return x.data_ptr()
