@@ -395,8 +395,7 @@ __global__ __launch_bounds__(256) void attn_join(Args a, int rows_max) {
 
 // How a call is cut. Sequences of at most 16 rows (tokens times group) go to the step kernel, longer ones
 // to the prompt kernel. Where max_q_len rules one of them out it is not launched; where sequences have 256
-// rows and more on average, the few short ones that may be among them go to the prompt kernel too (an
-// idle step kernel and its join cost 9 us).
+// rows and more on average, the few short ones that may be among them go to the prompt kernel too.
 struct Cut {
   bool step, prompt;
   int target;        // step: most ranges
@@ -418,12 +417,16 @@ Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t k
   if (p.prompt) {
     p.blocks = prompt_blocks(T, batch, group);
     const int64_t all = p.blocks * kv_heads;
-    p.splits = (int)(all >= 256 ? 1 : (512 / all > 16 ? 16 : 512 / all));
+    // one workgroup to a compute unit (two: 5 % faster to 20 % slower, for every part's results are written and read again)
+    p.splits = (int)(all > 128 ? 1 : (256 / all > 64 ? 64 : 256 / all));
     if (p.splits > 1) p.prompt_bytes = (size_t)(all * p.splits * 128 * (D + 2) * 4 + 255) & ~(size_t)255;
   }
   return p;
 }
 constexpr int kLeastTiles = 2;
+// (a tile takes a lone workgroup 1.7 us, most of it the wait for its loads: 20 rows over 900 tokens 36 us in parts of
+// eight tiles at least, 21.5 of four, 19 of three; 64 over 3000 29 of three, 37 of two)
+constexpr int kLeastPromptTiles = 3;
 
 template <class E, int D>
 hipError_t launch_step(const Args& a, const Cut& p, hipStream_t s) {
@@ -461,7 +464,13 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.window = p.window;
   a.full = p.full;
   a.max_q_len = (int)(p.max_q_len < p.T ? p.max_q_len : p.T);
-  const Cut plan = cut_of(p.c.batch, p.T, p.max_q_len, a.group, p.c.heads, p.c.dim);
+  Cut plan = cut_of(p.c.batch, p.T, p.max_q_len, a.group, p.c.heads, p.c.dim);
+  // Short sequences go along with the prompt kernel where none of its workgroups can have more than 64 tiles for
+  // that (one token's block costs it about what it costs the step kernel, and an idle step kernel and its join
+  // 10 to 15 us: 64 rows and 27 x 1 over 700 tokens 54 us with the step kernel, 36 without; 64 and 99 x 1 over 8000, one
+  // kv head, 124 and 96; 200 and 63 x 1 over 3000 98 and 108). A longer one would keep its workgroup for itself.
+  const int64_t most_tiles = ((int64_t)p.c.max_pages << p.c.shift) / kv::kTile + 1;
+  if (plan.prompt && most_tiles <= 64 * (int64_t)plan.splits) plan.step = false;
   a.least = kLeastTiles;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   hipError_t e = hipSuccess;
@@ -469,6 +478,7 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
     Args b = a;
     b.small = plan.step ? 16 : 0;
     b.splits = plan.splits;
+    b.least = kLeastPromptTiles;
     b.part_o = reinterpret_cast<float*>(ws + plan.step_bytes);
     b.part_ml = b.part_o + plan.blocks * p.c.heads * plan.splits * 128 * p.c.dim;
     e = launch_attn_prompt(dt, b, s);

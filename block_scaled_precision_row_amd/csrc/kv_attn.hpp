@@ -26,7 +26,7 @@ struct Args {
   int sign;             // of softmax_scale: q enters with it, scale2 is the magnitude (1 where it is 0)
   int max_q_len;
   int small;            // most rows (tokens times group) of a sequence that the step kernel takes
-  int target, least;    // step kernel: pieces of all sequences together, least tiles of a piece
+  int target, least;    // step kernel: pieces of all sequences together; least tiles of a piece, or of a prompt block's part
   int splits;           // prompt kernel: parts that a block's tokens are cut into
   float* part_o;        // partial results: step [piece][kv head][16][D], prompt [block][kv head][split][128][D]
   float* part_ml;       // their maxima (of scores times log2 e) and sums [...][2]

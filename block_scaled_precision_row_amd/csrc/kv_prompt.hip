@@ -65,9 +65,9 @@ __device__ __forceinline__ bool find_block(const Args& a, int64_t id, Block& o) 
   o.range = kv::seen_range(o.len, room_of(a.c), o.rows.n, i0, last - i0 + 1, a.window, a.full);
   return true;
 }
-// parts that a block's tiles are cut into: none of less than eight
+// parts that a block's tiles are cut into
 __device__ __forceinline__ int parts_of(const Args& a, int tiles) {
-  const int most = tiles / 8 < 1 ? 1 : tiles / 8;
+  const int most = tiles / a.least < 1 ? 1 : tiles / a.least;
   return a.splits < most ? a.splits : most;
 }
 

@@ -358,3 +358,19 @@ def test_int4_the_longest_rows(M, kind):
     # sums over a group, over a wave's groups and over the waves: (group + K / group + 4) roundings at most
     bound = u(dt) * np.abs(ref) + (group + K // group + 4) * 2.0 ** -24 * (40.0 if kind == "bf16" else 1.0) * size + 2.0 ** -25
     assert np.all(np.abs(y - ref) <= bound)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,page,window,full", [(64, 16, 0, False), (128, 64, 0, False), (128, 16, 333, False), (256, 256, 0, True)])
+def test_prompts_and_steps_in_one_call(D, page, window, full, kind):
+    """Chunks of a prompt and single tokens together, with tables wide enough for contexts that a workgroup must not walk
+    alone (then either kernel takes its part), and narrow ones."""
+    rows, lens = [40, 1, 3, 0, 2, 1, 1], [700, 900, 3, 50, 130, 1, 64]
+    c, cu, q = Cache(D + page, lens, 2, D, page), starts(rows), queries(D + 1, sum(rows) + 1, 8, D, kind)
+    for width in (c.table.shape[1], (1 << 19) // page):
+        table = np.full((len(rows), width), -1, np.int32)
+        table[:, :c.table.shape[1]] = c.table
+        c.table, narrow = table, c.table
+        y, lse = attention(c, cu, q, 40, softmax_scale=D ** -0.5, window=window, causal=not full)
+        c.table = narrow
+        check(c, cu, q, y, lse, D ** -0.5, window, full)
