@@ -12,9 +12,9 @@
 //
 // Bound by memory: 2 D bytes per token and kv head. Every wave streams tiles of 64 tokens of its own
 // through two LDS buffers (16 KB each for D 128), the next tile in flight while it works on one; two
-// workgroups of 64 KB to a compute unit. Loading the operands straight into registers, neighbouring lanes on
-// neighbouring rows, left the address unit with 16-byte pieces (64 sequences of 4000 to 8000 tokens,
-// 32 / 8 heads of 128: 205 us).
+// workgroups of 64 KB to a compute unit: 64 sequences of 4000 to 8000 tokens, 32 / 8 heads of 128, 773 MB in
+// 143 us, 5.4 TB/s, and 7 for the join. Loading the operands straight into registers, neighbouring lanes on
+// neighbouring rows, left the address unit with 16-byte pieces (205 us).
 #include "kv_attn.hpp"
 
 namespace bsq {

