@@ -401,9 +401,12 @@ struct Cut {
   int target;        // step: most ranges
   int rows;          // step: most rows of a sequence and kv head
   int64_t blocks;    // prompt: most blocks of 128 rows
-  int splits;
+  int splits, least; // prompt: most parts of a block, least tiles of a part
   size_t step_bytes, prompt_bytes;
 };
+// (a tile takes a lone workgroup 1.7 us, most of it the wait for its loads: 20 rows over 900 tokens 36 us in parts of
+// eight tiles at least, 21.5 of four, 19 of three; 64 over 3000 29 of three, 37 of two)
+constexpr int kLeastPromptTiles = 3;
 Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t kv_heads, int64_t D) {
   Cut p{};
   const int64_t most = (max_q_len < T ? max_q_len : T) * group;
@@ -417,16 +420,22 @@ Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t k
   if (p.prompt) {
     p.blocks = prompt_blocks(T, batch, group);
     const int64_t all = p.blocks * kv_heads;
-    // one workgroup to a compute unit (two: 5 % faster to 20 % slower, for every part's results are written and read again)
-    p.splits = (int)(all > 128 ? 1 : (256 / all > 64 ? 64 : 256 / all));
+    // One workgroup to a compute unit (two: 5 % faster to 20 % slower, for every part's results are written and read
+    // again). Blocks for more than half of them are cut in two where they are long, if two workgroups fit a unit (900
+    // rows over 6000 tokens, 8 heads of 64: 120 us whole, 104 cut; over 500 tokens 52 and 58; 600 over 2000, heads of 256, of
+    // which one fits: 118 and 131).
+    if (all <= 128) {
+      p.splits = (int)(256 / all > 64 ? 64 : 256 / all);
+      p.least = kLeastPromptTiles;
+    } else {
+      p.splits = all < 256 && D < 256 ? 2 : 1;
+      p.least = 16;
+    }
     if (p.splits > 1) p.prompt_bytes = (size_t)(all * p.splits * 128 * (D + 2) * 4 + 255) & ~(size_t)255;
   }
   return p;
 }
 constexpr int kLeastTiles = 2;
-// (a tile takes a lone workgroup 1.7 us, most of it the wait for its loads: 20 rows over 900 tokens 36 us in parts of
-// eight tiles at least, 21.5 of four, 19 of three; 64 over 3000 29 of three, 37 of two)
-constexpr int kLeastPromptTiles = 3;
 
 template <class E, int D>
 hipError_t launch_step(const Args& a, const Cut& p, hipStream_t s) {
@@ -471,6 +480,9 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   // kv head, 124 and 96; 200 and 63 x 1 over 3000 98 and 108). A longer one would keep its workgroup for itself.
   const int64_t most_tiles = ((int64_t)p.c.max_pages << p.c.shift) / kv::kTile + 1;
   if (plan.prompt && most_tiles <= 64 * (int64_t)plan.splits) plan.step = false;
+  // no parts, no join, where the table has no room for a block of several (a join costs 5 us)
+  if (plan.prompt && most_tiles / plan.least < plan.splits)
+    plan.splits = most_tiles < 2 * plan.least ? 1 : (int)(most_tiles / plan.least);
   a.least = kLeastTiles;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   hipError_t e = hipSuccess;
@@ -478,7 +490,7 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
     Args b = a;
     b.small = plan.step ? 16 : 0;
     b.splits = plan.splits;
-    b.least = kLeastPromptTiles;
+    b.least = plan.least;
     b.part_o = reinterpret_cast<float*>(ws + plan.step_bytes);
     b.part_ml = b.part_o + plan.blocks * p.c.heads * plan.splits * 128 * p.c.dim;
     e = launch_attn_prompt(dt, b, s);

@@ -374,3 +374,15 @@ def test_prompts_and_steps_in_one_call(D, page, window, full, kind):
         y, lse = attention(c, cu, q, 40, softmax_scale=D ** -0.5, window=window, causal=not full)
         c.table = narrow
         check(c, cu, q, y, lse, D ** -0.5, window, full)
+
+
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (128, 2200), (256, 0)])
+def test_chunks_of_many_heads(D, window):
+    """Blocks enough for more than half of the compute units, long enough to be cut in two. All heads hold the same: the
+    first is checked, the others have to be equal to it."""
+    H, rows, lens = 40, [500], [2600]
+    c, q = Cache(D, lens, 1, D, 64), queries(D + 1, 500, 1, D, "bf16")
+    dev = [gpu(a) for a in (c.lens, c.table)] + [gpu(a).expand(-1, H, *a.shape[2:]).contiguous() for a in (c.kc, c.vc, c.ks, c.vs)]
+    y, lse = L.bsq_attention_kv8(q.cuda().repeat(1, H, 1), gpu(starts(rows)), *dev, 500, window=window)
+    check(c, starts(rows), q, y[:, :1], lse[:, :1], D ** -0.5, window)
+    assert torch.equal(y, y[:, :1].repeat(1, H, 1)) and torch.equal(lse, lse[:, :1].repeat(1, H))
