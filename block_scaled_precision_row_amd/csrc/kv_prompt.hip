@@ -10,7 +10,7 @@
 // Bound by the vector instructions of the softmax and the decoding of E4M3 (two values an instruction), some 146 to
 // every 16 products of 32 rows and tokens, and next by the matrix cores. Tiles come into two LDS buffers, one
 // in flight while the other is worked on, with one barrier a tile. 3 sequences of 750 to 1500 rows over up to 6000
-// tokens, 32 / 8 heads of 128: 260 us, 783 TFLOP/s. Three waves a SIMD; K and V are read again by every block of
+// tokens, 32 / 8 heads of 128: 260 to 279 us from card to card, 783 to 731 TFLOP/s. Three waves a SIMD; K and V are read again by every block of
 // rows, from the L2 cache for the most part.
 #include <type_traits>
 
