@@ -394,8 +394,8 @@ __global__ __launch_bounds__(256) void attn_join(Args a, int rows_max) {
 }
 
 // How a call is cut. Sequences of at most 16 rows (tokens times group) go to the step kernel, longer ones
-// to the prompt kernel. Where max_q_len rules one of them out it is not launched; where sequences have 256
-// rows and more on average, the few short ones that may be among them go to the prompt kernel too.
+// to the prompt kernel. Where max_q_len, or a batch of one, rules one of them out it is not launched; nor the step
+// kernel where short sequences cannot keep the prompt kernel waiting (launch_attention).
 struct Cut {
   bool step, prompt;
   int target;        // step: most ranges
@@ -411,7 +411,7 @@ Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t k
   Cut p{};
   const int64_t most = (max_q_len < T ? max_q_len : T) * group;
   p.prompt = most > 16;
-  p.step = most <= 16 || (group <= 16 && T < 256 * batch);
+  p.step = most <= 16 || (group <= 16 && batch > 1);
   if (p.step) {
     p.target = (int)((512 + kv_heads - 1) / kv_heads);  // two workgroups to a compute unit
     p.rows = (int)(most < 16 ? most : 16);
@@ -476,8 +476,9 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   Cut plan = cut_of(p.c.batch, p.T, p.max_q_len, a.group, p.c.heads, p.c.dim);
   // Short sequences go along with the prompt kernel where none of its workgroups can have more than 64 tiles for
   // that (one token's block costs it about what it costs the step kernel, and an idle step kernel and its join
-  // 10 to 15 us: 64 rows and 27 x 1 over 700 tokens 54 us with the step kernel, 36 without; 64 and 99 x 1 over 8000, one
-  // kv head, 124 and 96; 200 and 63 x 1 over 3000 98 and 108). A longer one would keep its workgroup for itself.
+  // 5 to 15 us: 64 rows and 27 x 1 over 700 tokens 54 us with the step kernel, 36 without; 64 and 99 x 1 over 8000, one
+  // kv head, 124 and 96; 200 and 63 x 1 over 3000 98 and 108). A longer one would keep its workgroup for itself: 2048 rows
+  // and 7 x 1 over 8000 tokens 116 us with the step kernel, 242 without; with one of 60000 tokens 124 and 1689.
   const int64_t most_tiles = ((int64_t)p.c.max_pages << p.c.shift) / kv::kTile + 1;
   if (plan.prompt && most_tiles <= 64 * (int64_t)plan.splits) plan.step = false;
   // no parts, no join, where the table has no room for a block of several (a join costs 5 us)
