@@ -8,7 +8,7 @@
 // taken to be token 16 g + 4 j + r, so that over the four tiles a lane ends up with the 16 consecutive
 // tokens of granule l / 16: one page, one scale of K and of V to a lane, and P in the order in which the
 // second product wants its operand, without a shuffle or LDS. E4M3 becomes 16-bit exactly, two values an
-// instruction, V's scale in the conversion.
+// instruction; V's scale is in the weights (kv_attn.hpp).
 //
 // Bound by memory: 2 D bytes per token and kv head. Every wave streams tiles of 64 tokens of its own
 // through two LDS buffers (16 KB each for D 128), the next tile in flight while it works on one; two
@@ -146,9 +146,10 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
 
   const uint8_t* buf = smem + wave * 2 * tile_bytes(D);
   const uint32_t buf_lds = lds_offset(buf);
+  const int seen_lo = a.window > 0 ? row_at(a, 0, kvh, rows.n, len, room).lo : 0;  // the first token that any row sees
   Pages pages;
   if (count > 0) {
-    pages.load<D>(a.c, b, kvh, first, stride, all.hi);
+    pages.load<D>(a.c, b, kvh, first, stride, seen_lo, all.hi);
     loads.template issue<0, tile_loads(D)>(a.c, pages, 0, buf_lds);
   }
 
@@ -168,15 +169,17 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -INFINITY, l = 0.0f;
+  bool large = false;
 
   for (int it = 0; it < count; ++it) {
     const int t0 = first + stride * it, vt = t0 + 16 * g;
-    const int vid = pages.gone(it, g);
-    const float ks = pages.kscale(it, g) * a.scale2, vs = pages.vscale(it, g);
+    if ((it & 15) == 0) pages.settle();
+    const int vid = pages.gone(it, g), vs = pages.vshift(it, g);
+    const float ks = pages.kscale(it, g) * a.scale2;
     const uint8_t* kb = buf + (it & 1) * tile_bytes(D);
     const uint8_t* vb = kb + 64 * D;
     if (it + 1 < count) {
-      if (((it + 1) & 15) == 0) pages.load<D>(a.c, b, kvh, t0 + stride, stride, all.hi);
+      if (((it + 1) & 15) == 0) pages.load<D>(a.c, b, kvh, t0 + stride, stride, seen_lo, all.hi);
       wait_reads();
       loads.template issue<0, tile_loads(D)>(a.c, pages, it + 1, buf_lds + ((it + 1) & 1) * tile_bytes(D));
       wait_loads<tile_loads(D)>();
@@ -206,10 +209,11 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
     float top = x[0];
 #pragma unroll
     for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
+    top += (float)vs;
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     if (__ballot(outgrown(top, m))) {
-      const float mn = fmaxf(m, top);
+      const float mn = ceilf(fmaxf(m, top));
       const float alpha = __builtin_amdgcn_exp2f(m - finite_base(mn));
       l *= alpha;
 #pragma unroll
@@ -217,15 +221,24 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][r] *= alpha;
       m = mn;
+      large = __ballot(coarse(m)) != 0;
     }
-    const float base = finite_base(m);
-    Frag<E> p[2];
+    float base = finite_base(m);
+    if (large) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = coarse_score(x[j] - base, vs);
+      base = 0.0f;
+    }
+    base -= (float)(vs + kLift);
+    float sum = 0.0f;
+    Frag<Fp16> p[2];
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
       const float p0 = __builtin_amdgcn_exp2f(x[j] - base), p1 = __builtin_amdgcn_exp2f(x[j + 1] - base);
-      l += p0 + p1;
-      p[j >> 3].u[(j & 7) >> 1] = E::pack(p0, p1);
+      sum += p0 + p1;
+      p[j >> 3].u[(j & 7) >> 1] = Fp16::pack(p0, p1);
     }
+    l += ldexpf(sum, -vs);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       v4u v = *reinterpret_cast<const v4u*>(vb + 1024 * i + v_off);
@@ -235,8 +248,8 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
         poisoned = __ballot(bits != 0) != 0;
         if (poisoned) sh_nan[(wave * 16 + col) * 4 + g] = (uint16_t)bits;
       }
-      acc[i] = E::mfma(dec8<E>(v.x, v.y, vs), p[0].v, acc[i]);
-      acc[i] = E::mfma(dec8<E>(v.z, v.w, vs), p[1].v, acc[i]);
+      acc[i] = Fp16::mfma(dec8<Fp16>(v.x, v.y, 1.0f), p[0].v, acc[i]);
+      acc[i] = Fp16::mfma(dec8<Fp16>(v.z, v.w, 1.0f), p[1].v, acc[i]);
       if (poisoned) {  // the rows that see a NaN get it
         __threadfence_block();
         __builtin_amdgcn_wave_barrier();
@@ -252,11 +265,13 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
   // the waves' parts, joined in wave order
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
+  l *= 1.0f / (1 << kLift);
+  const float unit = pages.unit();
   __syncthreads();
   float* mine = sh_o + (wave * 16 + col) * (D + 4);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
-    *reinterpret_cast<float4*>(mine + 16 * i + 4 * g) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    *reinterpret_cast<float4*>(mine + 16 * i + 4 * g) = make_float4(acc[i][0] * unit, acc[i][1] * unit, acc[i][2] * unit, acc[i][3] * unit);
   if (g == 0) {
     sh_ml[(wave * 16 + col) * 2] = m;
     sh_ml[(wave * 16 + col) * 2 + 1] = l;

@@ -33,6 +33,7 @@ struct Args {
 };
 
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kLag = 4, kLift = 11;  // of the weights of the second product (below)
 
 __device__ __forceinline__ int room_of(const Cache& c) { return c.max_pages << c.shift; }
 
@@ -122,34 +123,49 @@ __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0
 
 // The granules of up to 16 tiles of a wave, lane l's granule l % 4 of tile l / 4: whether its page is present, where
 // its codes begin and their scales. An absent page's place is taken by page 0's, whose codes are hidden.
+//
+// V's scale, a power of two, does not enter the conversion of its codes (448 * 2^8 is an infinity in fp16, and would
+// reach rows that give it no weight), but the exponent of the probabilities, relative to a reference of the wave.
 struct Pages {
   int absent;  // -1: the page is absent, 0
   uint32_t k_lo, k_hi, v_lo, v_hi;
-  float ks, vs;
-  // tile i starts at token t0 + stride * i; tokens from `end` on are not looked up
+  float ks;
+  int vs;       // settled: the exponent of V's scale less the reference's
+  int ref = 0;  // the reference, a biased exponent: the largest of the first pages that are not all zeros
+  // tile i starts at token t0 + stride * i; granules that lie before `begin`, or from `end` on, are not looked up: no
+  // row sees them, and what an unused page happens to hold as its scales must not become the reference
   template <int D>
-  __device__ __forceinline__ void load(const Cache& c, int b, int head, int t0, int stride, int end) {
+  __device__ __forceinline__ void load(const Cache& c, int b, int head, int t0, int stride, int begin, int end) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)t0 + (int64_t)stride * (lane >> 2) + 16 * (lane & 3);
-    const int id = t < end ? kv::page_of(c, b, (int)t) : -1;
+    const int id = t + 16 > begin && t < end ? kv::page_of(c, b, (int)t) : -1;
     absent = id >> 31;
     const int64_t at = (int64_t)(id < 0 ? 0 : id) * c.heads + head, codes = (at << c.shift) * D;
     const int in = (int)t & ((1 << c.shift) - 1);
-    // (a scale that is not finite is not append's, but what an unused page happens to hold: its codes are hidden, as 0,
-    // and must not meet it)
     ks = c.ks[at];
-    vs = c.vs[at];
-    vs = fabsf(vs) <= 3.40282347e38f ? vs : 0.0f;
+    vs = __float_as_int(c.vs[at]);
     const int64_t k = codes + in * D, v = codes + in;
     k_lo = (uint32_t)k;
     k_hi = (uint32_t)(k >> 32);
     v_lo = (uint32_t)v;
     v_hi = (uint32_t)(v >> 32);
   }
+  // Makes `vs` of the scale that load() brought (apart, so that the tile's loads need not wait for it). A page of zeros
+  // may have any exponent: a low one, so that it does not outweigh others, but not so low that its tokens leave
+  // the sum.
+  __device__ __forceinline__ void settle() {
+    int e = vs >> 23 & 0xFF;
+    e = absent || e == 0xFF ? 0 : e;
+    if (ref == 0) ref = __builtin_amdgcn_readfirstlane((int)wave_max((float)e));
+    vs = e == 0 ? -40 : e - ref;
+  }
   static __device__ __forceinline__ int place(int tile, int gran) { return (tile & 15) * 4 + gran; }
   __device__ __forceinline__ int gone(int tile, int gran) const { return __shfl(absent, place(tile, gran), 64); }
   __device__ __forceinline__ float kscale(int tile, int gran) const { return __shfl(ks, place(tile, gran), 64); }
-  __device__ __forceinline__ float vscale(int tile, int gran) const { return __shfl(vs, place(tile, gran), 64); }
+  __device__ __forceinline__ int vshift(int tile, int gran) const { return __shfl(vs, place(tile, gran), 64); }
+  __device__ __forceinline__ float unit() const {  // of the accumulators: the reference, less the weights' factor
+    return __uint_as_float((uint32_t)ref << 23) * (1.0f / (1 << kLift));
+  }
 };
 
 // Issues loads [first, last) of a tile (its number `tile` in `pages`) into LDS at `lds`.
@@ -215,12 +231,19 @@ __device__ __forceinline__ unsigned long long seen_bits(const Row& row, int t0) 
   return s;
 }
 
-// The maximum that probabilities are taken against may lag behind the scores' by 2^8: they are then at most 256
-// (the same relative precision in 16 bits, and far from overflow in fp32 sums), and most tiles need no
-// rescaling of what is summed up.
-__device__ __forceinline__ bool outgrown(float top, float m) { return top > m + 8.0f; }
-// (a row that has seen nothing has -inf: its probabilities exp2(-inf - 0) are 0)
+// Weights w_j = 2^(x_j + v_j - N) enter the second product: x_j a score times log2 e, v_j the exponent of its V scale less the
+// reference. N is a whole number, so that v_j and it are taken off together without a rounding, and what is summed up is
+// rescaled exactly. It may lag behind the largest x + v by 2^4, in which most tiles need no rescaling; weights are
+// lifted by 2^11 and then at most 2^15, and the largest of a row is above 2^10: in fp16 (11 bits, more than bf16's 8, for
+// either type of tensors) they lose bits only below 2^-24 of it, and vanish below 2^-35. The sum of the probabilities takes w_j 2^-v_j.
+__device__ __forceinline__ bool outgrown(float top, float n) { return top > n + (float)kLag; }
+// (a row that has seen nothing has -inf: its weights exp2(-inf - 0) are 0)
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
+// from 2^22 on N and v_j are not taken off together: a step of fp32 might be more than v_j
+__device__ __forceinline__ bool coarse(float n) { return fabsf(n) >= 4194304.0f && n != -INFINITY; }
+
+// x - n, in that case, at most what keeps the weight within fp16 (NaN stays)
+__device__ __forceinline__ float coarse_score(float d, int vs) { return d > (float)(kLag - vs) ? (float)(kLag - vs) : d; }
 
 // eight query values with the softmax scale's sign (0: all zero)
 __device__ __forceinline__ uint4 signed_query(uint4 q, int sign) {

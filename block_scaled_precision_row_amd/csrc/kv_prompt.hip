@@ -96,6 +96,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
   const uint32_t lds = lds_offset(smem);
   const TileLoads<D, kv::kPrompt> loads(a.c);
   constexpr int kMine = tile_loads(D) / 4;  // a wave's share of a tile's loads
+  const int seen_lo = row_at(a, blk.r0, kvh, blk.rows.n, blk.len, room).lo;  // the first token that any row sees
   Pages pages;
   auto issue = [&](int tile, uint32_t at) __attribute__((always_inline)) {
     if (wave == 0) loads.template issue<0, kMine>(a.c, pages, tile, at);
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
     else loads.template issue<3 * kMine, 4 * kMine>(a.c, pages, tile, at);
   };
   if (count > 0) {
-    pages.load<D>(a.c, blk.b, kvh, first, kv::kTile, blk.range.hi);
+    pages.load<D>(a.c, blk.b, kvh, first, kv::kTile, seen_lo, blk.range.hi);
     issue(0, lds);
   }
 
@@ -130,9 +131,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
   float m = -INFINITY, l = 0.0f;
+  bool large = false;
 
   // Granules j and 2 + j of a tile; `masked`: some row of the block does not see some of the tile.
-  auto half_tile = [&](auto masked, int j, int t0, const uint8_t* kb, int vid, float ks, float vs)
+  auto half_tile = [&](auto masked, int j, int t0, const uint8_t* kb, int vid, float ks, int vs)
                        __attribute__((always_inline)) {
     const uint8_t* vb = kb + 64 * D;
     v16f s;
@@ -153,10 +155,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
     float top = s[0];
 #pragma unroll
     for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-    top *= ks;
+    top = fmaf(top, ks, (float)vs);
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     if (__ballot(outgrown(top, m))) {
-      const float mn = fmaxf(m, top);
+      const float mn = ceilf(fmaxf(m, top));
       const float alpha = __builtin_amdgcn_exp2f(m - finite_base(mn));
       l *= alpha;
 #pragma unroll
@@ -164,35 +166,46 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] *= alpha;
       m = mn;
+      large = __ballot(coarse(m)) != 0;
     }
-    const float base = finite_base(m);
-    Frag<E> p[2];  // tokens 8 i + 0..7 of the granule
+    float base = finite_base(m);
+    if (large) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = coarse_score(fmaf(s[r], ks, -base), vs);
+      ks = 1.0f;
+      base = 0.0f;
+    }
+    base -= (float)(vs + kLift);
+    float sum = 0.0f;
+    Frag<Fp16> p[2];  // tokens 8 i + 0..7 of the granule
 #pragma unroll
     for (int r = 0; r < 16; r += 2) {
       const float p0 = __builtin_amdgcn_exp2f(fmaf(s[r], ks, -base));
       const float p1 = __builtin_amdgcn_exp2f(fmaf(s[r + 1], ks, -base));
-      l += p0 + p1;
-      p[r >> 3].u[(r & 7) >> 1] = E::pack(p0, p1);
+      sum += p0 + p1;
+      p[r >> 3].u[(r & 7) >> 1] = Fp16::pack(p0, p1);
     }
+    l += ldexpf(sum, -vs);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const uint4 v = *reinterpret_cast<const uint4*>(vb + 2048 * i + v_off[j]);
-      acc[i] = E::mfma32(dec8<E>(v.x, v.y, vs), p[0].v, acc[i]);
-      acc[i] = E::mfma32(dec8<E>(v.z, v.w, vs), p[1].v, acc[i]);
+      acc[i] = Fp16::mfma32(dec8<Fp16>(v.x, v.y, 1.0f), p[0].v, acc[i]);
+      acc[i] = Fp16::mfma32(dec8<Fp16>(v.z, v.w, 1.0f), p[1].v, acc[i]);
     }
   };
   // waits for tile `it`, lets the next one start and gives the tile's pages and scales
-  auto advance = [&](int it, int t0, int(&vid)[2], float(&ks)[2], float(&vs)[2]) __attribute__((always_inline)) {
+  auto advance = [&](int it, int t0, int(&vid)[2], float(&ks)[2], int(&vs)[2]) __attribute__((always_inline)) {
+    if ((it & 15) == 0) pages.settle();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       vid[j] = pages.gone(it, 2 * h + j);
       ks[j] = pages.kscale(it, 2 * h + j) * a.scale2;
-      vs[j] = pages.vscale(it, 2 * h + j);
+      vs[j] = pages.vshift(it, 2 * h + j);
     }
     wait_loads<0>();
     __syncthreads();
     if (it + 1 < count) {
-      if (((it + 1) & 15) == 0) pages.load<D>(a.c, blk.b, kvh, t0 + kv::kTile, kv::kTile, blk.range.hi);
+      if (((it + 1) & 15) == 0) pages.load<D>(a.c, blk.b, kvh, t0 + kv::kTile, kv::kTile, seen_lo, blk.range.hi);
       issue(it + 1, lds + ((it + 1) & 1) * tile_bytes(D));
     }
   };
@@ -224,8 +237,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
       const int t0 = first + kv::kTile * it;
       const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
       const int vgran = pages.gone(it, loads.v_gran);
-      int vid[2];
-      float ks[2], vs[2];
+      int vid[2], vs[2];
+      float ks[2];
       advance(it, t0, vid, ks, vs);
       // V's codes that no row sees, and NaN codes, become 0 in LDS (a probability of 0 must not meet them); which
       // were NaN is kept for the rows that see them
@@ -257,8 +270,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
   for (int it = whole_begin; it < whole_end; ++it) {
     const int t0 = first + kv::kTile * it;
     const uint8_t* kb = smem + (it & 1) * tile_bytes(D);
-    int vid[2];
-    float ks[2], vs[2];
+    int vid[2], vs[2];
+    float ks[2];
     advance(it, t0, vid, ks, vs);
 #pragma unroll
     for (int j = 0; j < 2; ++j) half_tile(std::false_type(), j, t0, kb, vid[j], ks[j], vs[j]);
@@ -271,9 +284,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
       if (bad[i >> 1] >> (16 * (i & 1) + r) & 1) acc[i][r] = __builtin_nanf("");
 
   l += __shfl_xor(l, 32, 64);
+  l *= 1.0f / (1 << kLift);
+  const float unit = pages.unit();
   if (row.i < 0) return;
   if (parts == 1) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : unit / l;
     const int64_t out = (int64_t)(blk.rows.first + row.i);
     uint16_t* yr = a.y + out * a.yt + (int64_t)row.head * a.yh;
 #pragma unroll
@@ -290,7 +305,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
 #pragma unroll
       for (int r = 0; r < 16; r += 4)
         *reinterpret_cast<float4*>(a.part_o + slot * D + 32 * i + 2 * r + 4 * h) =
-            make_float4(acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]);
+            make_float4(acc[i][r] * unit, acc[i][r + 1] * unit, acc[i][r + 2] * unit, acc[i][r + 3] * unit);
     if (h == 0) {
       a.part_ml[slot * 2] = m;
       a.part_ml[slot * 2 + 1] = l;
