@@ -13,7 +13,7 @@
 // Bound by memory: 2 D bytes per token and kv head. Every wave streams tiles of 64 tokens of its own
 // through two LDS buffers (16 KB each for D 128), the next tile in flight while it works on one; two
 // workgroups of 64 KB to a compute unit: 64 sequences of 4000 to 8000 tokens, 32 / 8 heads of 128, 773 MB in
-// 143 us, 5.4 TB/s, and 7 for the join. Loading the operands straight into registers, neighbouring lanes on
+// 152 us, 5.1 TB/s, and 7 for the join. Loading the operands straight into registers, neighbouring lanes on
 // neighbouring rows, left the address unit with 16-byte pieces (205 us).
 #include "kv_attn.hpp"
 
@@ -231,12 +231,12 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
     }
     base -= (float)(vs + kLift);
     float sum = 0.0f;
-    Frag<Fp16> p[2];
+    Frag<Fp16> p[2], rest[2];
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
       const float p0 = __builtin_amdgcn_exp2f(x[j] - base), p1 = __builtin_amdgcn_exp2f(x[j + 1] - base);
       sum += p0 + p1;
-      p[j >> 3].u[(j & 7) >> 1] = Fp16::pack(p0, p1);
+      two_parts(p0, p1, p[j >> 3].u[(j & 7) >> 1], rest[j >> 3].u[(j & 7) >> 1]);
     }
     l += ldexpf(sum, -vs);
 #pragma unroll
@@ -248,8 +248,12 @@ __global__ __launch_bounds__(64 * step_waves(D)) void attn_step(Args a) {
         poisoned = __ballot(bits != 0) != 0;
         if (poisoned) sh_nan[(wave * 16 + col) * 4 + g] = (uint16_t)bits;
       }
-      acc[i] = Fp16::mfma(dec8<Fp16>(v.x, v.y, 1.0f), p[0].v, acc[i]);
-      acc[i] = Fp16::mfma(dec8<Fp16>(v.z, v.w, 1.0f), p[1].v, acc[i]);
+      const v8h v0 = dec8<Fp16>(v.x, v.y, 1.0f);
+      acc[i] = Fp16::mfma(v0, rest[0].v, acc[i]);
+      acc[i] = Fp16::mfma(v0, p[0].v, acc[i]);
+      const v8h v1 = dec8<Fp16>(v.z, v.w, 1.0f);
+      acc[i] = Fp16::mfma(v1, rest[1].v, acc[i]);
+      acc[i] = Fp16::mfma(v1, p[1].v, acc[i]);
       if (poisoned) {  // the rows that see a NaN get it
         __threadfence_block();
         __builtin_amdgcn_wave_barrier();

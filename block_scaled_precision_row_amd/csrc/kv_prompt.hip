@@ -7,11 +7,12 @@
 // be token 32 h + 16 j + 4 a + b, so that a lane holds the 16 consecutive tokens of granule 2 (l / 32) + j in
 // tile j: one scale of K and of V each, and P in the order in which the second product wants its operand.
 //
-// Bound by the vector instructions of the softmax and the decoding of E4M3 (two values an instruction), some 146 to
-// every 16 products of 32 rows and tokens, and next by the matrix cores. Tiles come into two LDS buffers, one
-// in flight while the other is worked on, with one barrier a tile. 3 sequences of 750 to 1500 rows over up to 6000
-// tokens, 32 / 8 heads of 128: 260 to 279 us from card to card, 783 to 731 TFLOP/s. Three waves a SIMD; K and V are read again by every block of
-// rows, from the L2 cache for the most part.
+// Bound by the vector instructions of the softmax and the decoding of E4M3 (two values an instruction), some 170 to
+// every 24 products of 32 rows and tokens, and by the matrix cores, a third of whose work is the weights' second part
+// (kv_attn.hpp). Tiles come into two LDS buffers, one in flight while the other is worked on, with one barrier a tile.
+// 3 sequences of 750 to 1500 rows over up to 6000 tokens, 32 / 8 heads of 128: 333 us, 613 TFLOP/s (281 with weights of 11
+// bits). Two waves a SIMD for heads of 128 (three: 63 registers spilled, 354 us), three for 64 (205 us for the same
+// sequences; two: 223). K and V are read again by every block of rows, from the L2 cache for the most part.
 #include <type_traits>
 
 #include "kv_attn.hpp"
@@ -76,7 +77,7 @@ __device__ __forceinline__ int parts_of(const Args& a, int tiles) {
 constexpr int prompt_lds(int D) { return 2 * tile_bytes(D) + D * 8; }  // buffers; the NaN map
 
 template <class E, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : (D == 128 ? 2 : 3)) void attn_prompt(Args a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   uint16_t* sh_nan = reinterpret_cast<uint16_t*>(smem + 2 * tile_bytes(D));  // [D][4 granules]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -177,20 +178,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 3) void attn_prompt(Args a) {
     }
     base -= (float)(vs + kLift);
     float sum = 0.0f;
-    Frag<Fp16> p[2];  // tokens 8 i + 0..7 of the granule
+    Frag<Fp16> p[2], rest[2];  // tokens 8 i + 0..7 of the granule
 #pragma unroll
     for (int r = 0; r < 16; r += 2) {
       const float p0 = __builtin_amdgcn_exp2f(fmaf(s[r], ks, -base));
       const float p1 = __builtin_amdgcn_exp2f(fmaf(s[r + 1], ks, -base));
       sum += p0 + p1;
-      p[r >> 3].u[(r & 7) >> 1] = Fp16::pack(p0, p1);
+      two_parts(p0, p1, p[r >> 3].u[(r & 7) >> 1], rest[r >> 3].u[(r & 7) >> 1]);
     }
     l += ldexpf(sum, -vs);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const uint4 v = *reinterpret_cast<const uint4*>(vb + 2048 * i + v_off[j]);
-      acc[i] = Fp16::mfma32(dec8<Fp16>(v.x, v.y, 1.0f), p[0].v, acc[i]);
-      acc[i] = Fp16::mfma32(dec8<Fp16>(v.z, v.w, 1.0f), p[1].v, acc[i]);
+      const v8h v0 = dec8<Fp16>(v.x, v.y, 1.0f);
+      acc[i] = Fp16::mfma32(v0, rest[0].v, acc[i]);
+      acc[i] = Fp16::mfma32(v0, p[0].v, acc[i]);
+      const v8h v1 = dec8<Fp16>(v.z, v.w, 1.0f);
+      acc[i] = Fp16::mfma32(v1, rest[1].v, acc[i]);
+      acc[i] = Fp16::mfma32(v1, p[1].v, acc[i]);
     }
   };
   // waits for tile `it`, lets the next one start and gives the tile's pages and scales

@@ -159,9 +159,9 @@ bsq_status bsq_kv_append(bsq_dtype dtype, const bsq_kv8_cache* cache, const int3
  * does not reach it, be it NaN or beyond the range of `dtype`. Scores, the
  * running maximum and sum and the output are held in fp32. V's codes enter the
  * second product as they are, and each token's weight, its probability times its
- * page's scale, in fp16 with an exponent of the row's own: 11 bits, fewer below
- * 2^-24 of the row's largest weight and none below 2^-35. (The V scales of pages
- * that one row sees may be up to 2^100 apart.)
+ * page's scale, as the sum of two fp16 numbers with an exponent of the row's own:
+ * 21 bits, fewer where that would be below 2^-35 of the row's largest weight.
+ * (The V scales of pages that one row sees may be up to 2^100 apart.)
  *   q, y [T][q_heads][head_dim] of `dtype` (BSQ_BF16 or BSQ_FP16): 16-byte
  *     aligned, strides multiples of 8 (0 <= stride < 2^40), y's rows must not
  *     overlap; lse [T][q_heads] fp32 or NULL

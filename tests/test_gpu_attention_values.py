@@ -2,10 +2,11 @@
 scales far apart, pages of zeros, long flat tails, scores past 2^24.
 
 Tolerances, from the arithmetic (u(t) = eps(t) / 2). The second product takes V's codes as they are (exact in fp16) and
-weights w = p * (V's page scale) in fp16, in units of a power of two N that the largest weight of the row is at least half
-of; weights are at most 2^15 and the largest is above 2^10. So y errs by u(t) |y|; by a rounding of each weight to
-fp16, P_REL w, which for weights below fp16's normal range is 2^-25, at most 2^-35 of the largest weight W, so 2^-35 W sum |code| /
-sum p; by the scores, (D + 4) 2^-24 max sum |q k| scale, in numerator and denominator alike; 2^-20 for exp2 and its argument; n
+weights w = p * (V's page scale) as the sum of two fp16 numbers, in units of a power of two N that the largest weight of the
+row is at least half of; weights are at most 2^15 and the largest is above 2^10. The first part is off by less than 2^-10 w
+(towards zero), the second by half a step of what is left, so y errs by u(t) |y|; by P_REL w = 2^-10 2^-11 w of each weight,
+which for parts below fp16's normal range is 2^-25, at most 2^-35 of the largest weight W, so 2^-35 W sum |code| / sum p;
+by the scores, (D + 4) 2^-24 max sum |q k| scale, in numerator and denominator alike; 2^-20 for exp2 and its argument; n
 2^-24 for the sums. lse errs by the scores, n 2^-24, 2^-20, and a rounding of N and of the log of the sum, which cancel where
 scales of pages are 2^s apart: 2^-23 (|lse| + s).
 """
@@ -22,7 +23,7 @@ pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
     from block_scaled_precision_row_amd import _lib as L
 
-P_REL = 2.0 ** -10   # a weight's rounding to fp16, in any direction
+P_REL = 2.0 ** -21   # what two fp16 parts leave of a weight
 
 
 def queries(seed, T, Hq, D, kind, size=1.0):
@@ -235,3 +236,15 @@ def test_scores_past_2_to_24(rows, kind):
     want = serve.gather(c.vc, c.vs, c.table[0], 200, 0, True)[0][67]
     assert np.all(np.abs(f64(y) - want) <= u(q.dtype) * np.abs(want) + P_REL * np.abs(want))
     assert np.all(np.abs(f64(lse) - 2e9) <= 2.0 ** -20 * 2e9)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,lens,D", [([1, 1], [700, 33], 128), ([3], [500], 64), ([1], [600], 256), ([60], [600], 64), ([40], [500], 128),
+                                         ([20], [300], 256)])
+def test_weights_in_as_many_bits_as_their_sum(rows, lens, D, kind):
+    """Scores near 1, values of either sign that cancel for the most part: y's own rounding is far below sum p |v|, of which
+    weights in 11 bits would cost 2^-12 here and there."""
+    c, cu, q = Cache(77, lens, 1, D, 16), starts(rows), queries(78, sum(rows), 4, D, kind, 0.05)
+    c.vs[:] = 0.5
+    y, lse = attend(c, cu, q, max(rows), softmax_scale=D ** -0.5)
+    check(c, cu, q, y, lse, D ** -0.5)
