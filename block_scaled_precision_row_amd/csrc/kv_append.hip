@@ -35,27 +35,20 @@ struct Args {
   uint64_t page_share;  // workgroups of pages in all, times 2^32, rounded up
 };
 
-// The last b in [0, batch) with at(b), -1 if none; at holds for a prefix. 256 candidates a step, four
-// independent loads to a lane: the search is part of a decode step's chain of dependent loads, and batches of
-// up to 256 take one round trip.
+// The last b in [0, batch) with at(b), -1 if none. 256 candidates a step, four independent loads to a lane: the
+// search is part of a decode step's chain of dependent loads, and batches of up to 256 take one round trip.
 template <class At>
 __device__ __forceinline__ int last_sequence(int batch, At at) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, n = batch;
-  while (true) {
-    const int step = (n + 255) >> 8;
+  return __builtin_amdgcn_readfirstlane(kv::last_of<256>(batch, [&](int lo, int step, int n) {
     int cnt = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = (lane + 64 * j) * step;
       cnt += __popcll(__ballot(i < n && at(lo + (i < n ? i : 0))));
     }
-    if (cnt == 0) return -1;
-    const int skip = (cnt - 1) * step;
-    lo += skip;
-    n = step < n - skip ? step : n - skip;
-    if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
-  }
+    return cnt;
+  }));
 }
 
 // Elements of unit u (16 of a head's D): two pieces of eight, from e0 and e1 on, and whether they are rotated.

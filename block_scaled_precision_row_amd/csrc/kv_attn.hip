@@ -437,7 +437,7 @@ Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t k
     p.step_bytes = (size_t)(2 * p.target * kv_heads * 16 * (D + 2) * 4 + 255) & ~(size_t)255;
   }
   if (p.prompt) {
-    p.blocks = prompt_blocks(T, batch, group);
+    p.blocks = kv::prompt_blocks(T, batch, group);
     const int64_t all = p.blocks * kv_heads;
     // One workgroup to a compute unit (two: 5 % faster to 20 % slower, for every part's results are written and read
     // again). Blocks for more than half of them are cut in two where they are long, if two workgroups fit a unit (900
@@ -486,7 +486,7 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.lse = p.lse;
   a.q_heads = p.q_heads;
   a.group = p.q_heads / p.c.heads;
-  a.group_inverse = (uint32_t)((((uint64_t)1 << 32) + a.group - 1) / a.group);
+  a.group_inverse = kv::inverse_of(a.group);
   a.sign = p.scale < 0.0f ? -1 : (p.scale > 0.0f ? 1 : 0);
   a.scale2 = a.sign == 0 ? 1.0f : (a.sign < 0 ? -p.scale : p.scale) * 1.44269504088896340736f;
   a.window = p.window;

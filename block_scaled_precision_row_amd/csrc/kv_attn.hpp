@@ -19,7 +19,7 @@ struct Args {
   float* lse;
   int64_t qt, qh, yt, yh;
   int q_heads, group;
-  uint32_t group_inverse;  // ceil(2^32 / group), for groups above 1
+  uint32_t group_inverse;  // kv::inverse_of(group)
   float scale2;  // |softmax_scale| * log2(e)
   int64_t window;
   bool full;
@@ -45,11 +45,11 @@ struct Row {
 };
 // (`few`: R below 16, divided by a multiplication)
 __device__ __forceinline__ Row row_at(const Args& a, int R, int kvh, int n, int len, int room, bool few = false) {
+  const kv::RowPlace at = kv::row_place(R, a.group, few ? a.group_inverse : 0u, kvh, n, a.max_q_len);
   Row r;
-  r.i = !few ? R / a.group : (a.group == 1 ? R : (int)__umulhi((uint32_t)R, a.group_inverse));
-  r.head = kvh * a.group + (R - r.i * a.group);
-  if (r.i >= n || r.i >= a.max_q_len) {
-    r.i = -1;
+  r.i = at.i;
+  r.head = at.head;
+  if (r.i < 0) {
     r.lo = 0;
     r.hi = 0x7FFFFFFF;  // (computed, never stored: it must not ask for a mask)
     return r;
@@ -268,6 +268,5 @@ __device__ __forceinline__ uint4 signed_query(uint4 q, int sign) {
 
 // the prompt kernel (kv_prompt.hip): sequences of more than `a.small` rows; blocks of 128 rows
 hipError_t launch_attn_prompt(bsq_dtype dt, const attn::Args& a, hipStream_t s);
-int64_t prompt_blocks(int64_t T, int64_t batch, int64_t group);
 
 }  // namespace bsq

@@ -38,6 +38,22 @@ BSQ_HD Rows rows_of(const int32_t* cu, int b, int64_t T) {
   return Rows{lo, hi - lo};
 }
 
+// The last b in [0, n) for which a condition holds that holds for a prefix, -1 if for none: `count(lo, step, n)` says
+// for how many of lo, lo + step, ... (below lo + n, at most WIDTH of them) it does. Where it holds for no prefix
+// (starts that decrease) the result is some b in range, and what is made of it has to be checked.
+template <int WIDTH, class Count>
+BSQ_HD int last_of(int n, Count count) {
+  int lo = 0;
+  while (true) {
+    const int step = (n + WIDTH - 1) / WIDTH, cnt = count(lo, step, n);
+    if (cnt == 0) return -1;
+    const int skip = (cnt - 1) * step;
+    lo += skip;
+    n = step < n - skip ? step : n - skip;
+    if (step == 1) return lo;
+  }
+}
+
 // the page of sequence b's token t, -1 where it is absent
 BSQ_HD int page_of(const Cache& c, int b, int t) {
   const int j = t >> c.shift;
@@ -70,6 +86,7 @@ BSQ_HD Touched touched_page(const Cache& c, const int32_t* cu, int b, int64_t j,
   const Rows r = rows_of(cu, b, T);
   const int64_t len = c.lens[b], past = len - r.n;
   if (r.n == 0 || past < 0) return none;
+  if (j < 0) return none;  // (starts that decrease)
   const int64_t start = ((past >> c.shift) + j) << c.shift;
   if (start >= len || (start >> c.shift) >= c.max_pages) return none;
   const int64_t lo = past > start ? past : start;
@@ -106,6 +123,33 @@ BSQ_HD int range_of(int chunk, int x) { return (int)((unsigned)x / (unsigned)chu
 // A sequence that lies in several ranges leaves a partial result in each: at most one range begins inside
 // it or with it (slot 2 r) for every one but the first, which may hold others before it (slot 2 r + 1).
 BSQ_HD int64_t partial_slot(int r, bool at_begin) { return 2 * (int64_t)r + (at_begin ? 0 : 1); }
+
+// ---- prompts: blocks of 128 rows (token, query head of the group) of a sequence and kv head -------
+// Blocks of sequence b start at first_block(b) = cu[b] * group / 128 + b; n tokens need at most
+// n * group / 128 + 1 of them.
+constexpr int kBlock = 128;
+BSQ_HD int64_t first_block(const int32_t* cu, int b, int64_t T, int group) {
+  const int t = cu[b];
+  return (int64_t)(t < 0 ? 0 : (t > (int)T ? (int)T : t)) * group / kBlock + b;
+}
+BSQ_HD int64_t prompt_blocks(int64_t T, int64_t batch, int64_t group) { return T * group / kBlock + batch; }
+// first row of block `id` among the n * group of sequence b; -1 where the block has none (of max_q_len tokens), or the
+// sequence has at most `small` rows
+BSQ_HD int block_row(const int32_t* cu, int b, const Rows& rows, int64_t T, int group, int64_t id, int small, int max_q_len) {
+  const int64_t all = (int64_t)rows.n * group, r0 = (id - first_block(cu, b, T, group)) * kBlock;
+  if (r0 < 0) return -1;  // (starts that decrease)
+  return all <= small || r0 >= all || r0 / group >= max_q_len ? -1 : (int)r0;
+}
+// token (of the sequence's n, -1 for none) and query head of row R >= 0. `inverse`: ceil(2^32 / group), with which
+// rows below 16 are divided by a group of at most 16; 0: any row and group
+struct RowPlace {
+  int i, head;
+};
+BSQ_HD uint32_t inverse_of(int group) { return group == 1 ? 1u : (uint32_t)((((uint64_t)1 << 32) + group - 1) / group); }
+BSQ_HD RowPlace row_place(int R, int group, uint32_t inverse, int kvh, int n, int max_q_len) {
+  const int i = inverse == 0 ? R / group : (group == 1 ? R : (int)((uint64_t)(uint32_t)R * inverse >> 32));
+  return RowPlace{i >= n || i >= max_q_len ? -1 : i, kvh * group + (R - i * group)};
+}
 
 // A prompt block's tiles are cut into equal parts.
 BSQ_HD int piece_begin(int tiles, int pieces, int i) { return (int)((int64_t)tiles * i / pieces); }

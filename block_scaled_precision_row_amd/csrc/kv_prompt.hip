@@ -23,27 +23,15 @@ namespace {
 
 using namespace attn;
 
-constexpr int kBlock = 128;
+using kv::kBlock;
 
-// Blocks of sequence b start at first_block(b) = cu[b] * group / 128 + b; n tokens need at most
-// n * group / 128 + 1 of them.
-__device__ __forceinline__ int64_t first_block(const Args& a, int b) {
-  const int t = a.cu[b], T = (int)a.T;
-  return (int64_t)(t < 0 ? 0 : (t > T ? T : t)) * a.group / kBlock + b;
-}
 // the last b whose first block is at most `id`, -1 if none: 64 candidates a step
 __device__ __forceinline__ int block_sequence(const Args& a, int64_t id) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, n = a.c.batch;
-  while (true) {
-    const int step = (n + 63) >> 6;
-    const bool in = lane * step < n && first_block(a, lo + lane * step) <= id;
-    const int cnt = __popcll(__ballot(in));
-    if (cnt == 0) return -1;
-    lo += (cnt - 1) * step;
-    n = step < n - (cnt - 1) * step ? step : n - (cnt - 1) * step;
-    if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
-  }
+  return __builtin_amdgcn_readfirstlane(kv::last_of<64>(a.c.batch, [&](int lo, int step, int n) {
+    const bool in = lane * step < n && kv::first_block(a.cu, lo + lane * step, a.T, a.group) <= id;
+    return (int)__popcll(__ballot(in));
+  }));
 }
 
 // a block's rows and the tokens they see
@@ -57,13 +45,12 @@ __device__ __forceinline__ bool find_block(const Args& a, int64_t id, Block& o) 
   o.b = block_sequence(a, id);
   if (o.b < 0) return false;
   o.rows = kv::rows_of(a.cu, o.b, a.T);
-  const int64_t all = (int64_t)o.rows.n * a.group, r0 = (id - first_block(a, o.b)) * kBlock;
-  if (all <= a.small || r0 >= all || r0 / a.group >= a.max_q_len) return false;
-  o.r0 = (int)r0;
+  o.r0 = kv::block_row(a.cu, o.b, o.rows, a.T, a.group, id, a.small, a.max_q_len);
+  if (o.r0 < 0) return false;
   const int len = a.c.lens[o.b];
   o.len = len < 0 ? 0 : len;
   const int i0 = o.r0 / a.group;
-  const int64_t i1 = (r0 + kBlock - 1) / a.group;
+  const int64_t i1 = ((int64_t)o.r0 + kBlock - 1) / a.group;
   const int last = i1 < o.rows.n - 1 ? (int)i1 : o.rows.n - 1;
   o.range = kv::seen_range(o.len, room_of(a.c), o.rows.n, i0, last - i0 + 1, a.window, a.full);
   return true;
@@ -358,7 +345,7 @@ hipError_t launch(const Args& a, hipStream_t s) {
   static std::atomic<unsigned long long> raised{0};
   hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(attn_prompt<E, D>), prompt_lds(D), raised);
   if (e != hipSuccess) return e;
-  const unsigned blocks = (unsigned)(prompt_blocks(a.T, a.c.batch, a.group) * a.c.heads);
+  const unsigned blocks = (unsigned)(kv::prompt_blocks(a.T, a.c.batch, a.group) * a.c.heads);
   hipLaunchKernelGGL((attn_prompt<E, D>), dim3(blocks, (unsigned)a.splits), dim3(256),
                      prompt_lds(D), s, a);
   e = hipGetLastError();
@@ -368,8 +355,6 @@ hipError_t launch(const Args& a, hipStream_t s) {
 }
 
 }  // namespace
-
-int64_t prompt_blocks(int64_t T, int64_t batch, int64_t group) { return T * group / kBlock + batch; }
 
 hipError_t launch_attn_prompt(bsq_dtype dt, const attn::Args& a, hipStream_t s) {
   const bool half = dt == BSQ_FP16;

@@ -104,6 +104,8 @@ bsq_status bsq_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t 
  * 0 and not decreasing), and they are its last ones: row cu_seqlens[b] + i has
  * position seq_lens[b] - n_b + i, n_b = cu_seqlens[b + 1] - cu_seqlens[b]. Rows
  * from cu_seqlens[batch] on belong to no sequence: not written, and without effect.
+ * Where cu_seqlens decreases or leaves [0, T], which rows and pages of the call's
+ * tensors are read and written, and with what, is not defined.
  */
 typedef struct {
   uint8_t* k;
