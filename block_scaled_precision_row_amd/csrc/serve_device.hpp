@@ -86,14 +86,20 @@ __device__ __forceinline__ void store8<Fp32>(float* p, const float (&f)[8]) {
 }
 
 // Cos and sin of position * w, times `factor`, in 64 bits (whose vector instructions take as long as those of 32
-// here): the angle as a fraction of a turn (a position of 10^6 keeps 10^-10 of one), less whole quarters, and the
-// Taylor series on what is left, at most pi / 4: the first terms left out are x^15 / 15! and x^14 / 14!, below 4e-13.
+// here): the angle as a fraction of a turn, less whole quarters, and the Taylor series on what is left, at most pi / 4:
+// the first terms left out are x^15 / 15! and x^14 / 14!, below 4e-13. The product of position and w and its part of a turn
+// are formed with what their roundings leave (1 / 2 pi in two parts), so that the fraction is off by 2^-53 of a turn at
+// any position below 2^53; without it by 2^-53 of all turns, 2^-22 at 2^31, of which one key's code in a million comes out
+// wrong, and everything at 2^53.
 struct Turn {
   double c, s;
 };
 __device__ __forceinline__ Turn rope_turn(double position, float w, float factor) {
-  double t = position * (double)w * 0.15915494309189533577;
-  t -= rint(t);
+  const double a0 = position * (double)w, a1 = fma(position, (double)w, -a0);
+  constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18;
+  double t = a0 * kTurn;
+  const double rest = fma(a0, kTurn, -t) + fma(a0, kTurnRest, a1 * kTurn);
+  t = t - rint(t) + rest;
   const double quarter = rint(4.0 * t);
   const double x = fma(quarter, -0.25, t) * 6.283185307179586476925, z = x * x;
   double s = fma(z, 1.0 / 6227020800.0, -1.0 / 39916800.0), c = fma(z, 1.0 / 479001600.0, -1.0 / 3628800.0);
