@@ -225,7 +225,8 @@ bsq_status bsq_attention_kv8(bsq_dtype dtype, const bsq_kv8_cache* cache, const 
   a.y = bsq::Strided{y, y_stride_t, y_stride_h};
   a.q_heads = (int)q_heads;
   a.scale = softmax_scale;
-  a.window = window;
+  // (positions are below 2^31: a window of 2^32 hides nothing, and a wider one must not take them past 64 bits)
+  a.window = window < (int64_t)1 << 32 ? window : (int64_t)1 << 32;
   a.full = (flags & BSQ_ATTN_FULL) != 0;
   a.lse = lse;
   return finish(bsq::launch_attention(dtype, a, workspace, stream));
