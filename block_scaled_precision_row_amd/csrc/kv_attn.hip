@@ -487,8 +487,8 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.q_heads = p.q_heads;
   a.group = p.q_heads / p.c.heads;
   a.group_inverse = kv::inverse_of(a.group);
-  a.sign = p.scale < 0.0f ? -1 : (p.scale > 0.0f ? 1 : 0);
-  a.scale2 = a.sign == 0 ? 1.0f : (a.sign < 0 ? -p.scale : p.scale) * 1.44269504088896340736f;
+  a.sign = p.scale < 0.0f ? -1 : 1;
+  a.scale2 = fabsf(p.scale) * 1.44269504088896340736f;
   a.window = p.window;
   a.full = p.full;
   a.max_q_len = (int)(p.max_q_len < p.T ? p.max_q_len : p.T);

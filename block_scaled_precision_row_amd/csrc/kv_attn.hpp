@@ -23,7 +23,7 @@ struct Args {
   float scale2;  // |softmax_scale| * log2(e)
   int64_t window;
   bool full;
-  int sign;             // of softmax_scale: q enters with it, scale2 is the magnitude (1 where it is 0)
+  int sign;             // of softmax_scale, -1 or 1: q enters with it, scale2 is the magnitude
   int max_q_len;
   int small;            // most rows (tokens times group) of a sequence that the step kernel takes
   int target, least;    // step kernel: pieces of all sequences together; least tiles of a piece, or of a prompt block's part
@@ -258,10 +258,10 @@ __device__ __forceinline__ void two_parts(float a, float b, uint32_t& first, uin
   rest = r.u;
 }
 
-// eight query values with the softmax scale's sign (0: all zero)
+// eight query values with the softmax scale's sign
 __device__ __forceinline__ uint4 signed_query(uint4 q, int sign) {
-  const uint32_t flip = sign < 0 ? 0x80008000u : 0u, keep = sign == 0 ? 0u : 0xFFFFFFFFu;
-  return make_uint4((q.x ^ flip) & keep, (q.y ^ flip) & keep, (q.z ^ flip) & keep, (q.w ^ flip) & keep);
+  const uint32_t flip = sign < 0 ? 0x80008000u : 0u;
+  return make_uint4(q.x ^ flip, q.y ^ flip, q.z ^ flip, q.w ^ flip);
 }
 
 }  // namespace attn

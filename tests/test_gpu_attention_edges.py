@@ -24,3 +24,19 @@ def test_the_widest_windows_hide_nothing(rows, lens, window):
     want = attend(c, cu, q, max(rows), softmax_scale=0.2)
     got = attend(c, cu, q, max(rows), softmax_scale=0.2, window=window)
     assert torch.isfinite(want[1]).any() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,lens", [([1, 1], [70, 300]), ([3], [90]), ([40], [200])])
+def test_a_scale_of_zero_is_a_product_like_any_other(rows, lens, kind):
+    """Rows of finite queries take the mean, a row with a NaN or an infinity in its query is NaN (0 times it is)."""
+    c, cu = Cache(5, lens, 1, 64, 16), starts(rows)
+    q = torch.from_numpy(np.random.default_rng(6).standard_normal((sum(rows), 4, 64))).to(DTYPES[kind])
+    want, want_l = attend(c, cu, q, max(rows), softmax_scale=0.0)
+    assert torch.isfinite(want).all()
+    q[0, 1, 7], q[-1, 2, 40] = float("nan"), float("inf")
+    y, lse = attend(c, cu, q, max(rows), softmax_scale=0.0)
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool)
+    bad[0, 1] = bad[-1, 2] = True
+    assert torch.isnan(y.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
+    assert torch.equal(y.cpu()[~bad], want.cpu()[~bad]) and torch.equal(lse.cpu()[~bad], want_l.cpu()[~bad])
