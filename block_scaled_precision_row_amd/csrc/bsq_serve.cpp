@@ -201,7 +201,7 @@ bsq_status bsq_attention_kv8(bsq_dtype dtype, const bsq_kv8_cache* cache, const 
   if (!is16(dtype) || (flags & ~BSQ_ATTN_FULL)) return BSQ_ERR_ARG;
   bsq_status st = check_cache_shape(cache, T);
   if (st != BSQ_OK) return st;
-  if (!std::isfinite(softmax_scale) || window < 0 || (window > 0 && (flags & BSQ_ATTN_FULL))) return BSQ_ERR_ARG;
+  if (!std::isfinite(softmax_scale * 1.44269504088896340736f) || window < 0 || (window > 0 && (flags & BSQ_ATTN_FULL))) return BSQ_ERR_ARG;
   if (!attention_shape(cache->batch, T, max_q_len, q_heads, cache->kv_heads, cache->head_dim)) return BSQ_ERR_SHAPE;
   if (cache->batch * (cache->max_pages * cache->page_size / 64 + 1) >= (int64_t)1 << 31) return BSQ_ERR_SHAPE;
   if (!wide_strides(q_stride_t, q_stride_h) || !wide_strides(y_stride_t, y_stride_h)) return BSQ_ERR_SHAPE;

@@ -170,7 +170,7 @@ bsq_status bsq_kv_append(bsq_dtype dtype, const bsq_kv8_cache* cache, const int3
  *   max_q_len: at least the largest n_b (1 for a decode step; T always does);
  *     of a longer sequence only rows up to max_q_len are written
  *   window >= 0; BSQ_ERR_ARG for a window with BSQ_ATTN_FULL, an unknown flag
- *     or a softmax_scale that is not finite
+ *     or a softmax_scale that is not finite, also times log2(e) (in fp32)
  * A sequence with seq_lens[b] < n_b has negative positions: those rows see
  * nothing (with BSQ_ATTN_FULL they see all). Tokens past max_pages count as
  * absent. The scales of pages that a row sees have to be what bsq_kv_append
