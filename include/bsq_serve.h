@@ -198,7 +198,7 @@ bsq_status bsq_attention_kv8(bsq_dtype dtype, const bsq_kv8_cache* cache, const 
  *   x [M][ldx], y [M][ldy] of `dtype` (BSQ_BF16 or BSQ_FP16)
  *   w [N][K/2], element 2j in the low nibble of byte j
  *   w_scale [N][K/group] of `dtype`; w_zero [N][K/group] uint8 (0..255) or NULL
- * group 32, 64 or 128, K % group == 0; M <= 2^20 - 16, N < 2^27, K <= 2^20; shape,
+ * group 32, 64 or 128, K % group == 0; M <= 2^20 - 16, N <= 2^27 - 16, K <= 2^20; shape,
  * ld and alignment rules of bsq.h (w_scale 2-byte, w_zero 1-byte aligned). Sums
  * are of x c (BSQ_BF16: of x (c + 128), which x (z + 128) is taken from), so
  * they must not leave fp32's range: with |x| below 2^90 none does.
