@@ -424,7 +424,7 @@ struct Cut {
   size_t step_bytes, prompt_bytes;
 };
 // (a tile takes a lone workgroup 1.7 us, most of it the wait for its loads: 20 rows over 900 tokens 36 us in parts of
-// eight tiles at least, 21.5 of four, 19 of three; 64 over 3000 29 of three, 37 of two)
+// eight tiles at least, 22.6 of four, 20.3 of three, 21.2 of two; 64 over 3000 28.0 of three, 30.5 of two)
 constexpr int kLeastPromptTiles = 3;
 Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t kv_heads, int64_t D) {
   Cut p{};
@@ -439,16 +439,17 @@ Cut cut_of(int64_t batch, int64_t T, int64_t max_q_len, int64_t group, int64_t k
   if (p.prompt) {
     p.blocks = kv::prompt_blocks(T, batch, group);
     const int64_t all = p.blocks * kv_heads;
-    // One workgroup to a compute unit (two: 5 % faster to 20 % slower, for every part's results are written and read
-    // again). Blocks for more than half of them are cut in two where they are long, if two workgroups fit a unit (900
-    // rows over 6000 tokens, 8 heads of 64: 120 us whole, 104 cut; over 500 tokens 52 and 58; 600 over 2000, heads of 256, of
-    // which one fits: 118 and 131).
+    // One workgroup to a compute unit (two: 18 % faster to 25 % slower, for every part's results are written and read
+    // again: 64 rows and 99 x 1 over 8000 tokens 95 us against 117, 100 rows over 8000, two heads of 64, 46 against 37). Blocks
+    // for more than half of them are cut in two where they are long, if two workgroups fit a unit (900 rows over
+    // 6000 tokens, 32 / 8 heads of 64: 119 us whole, 101 cut, of 128: 160 and 154; over 2000 of 64 46 and 51, of 128 62 and 69;
+    // 600 over 2000, heads of 256, of which one fits: 123 and 131).
     if (all <= 128) {
       p.splits = (int)(256 / all > 64 ? 64 : 256 / all);
       p.least = kLeastPromptTiles;
     } else {
       p.splits = all < 256 && D < 256 ? 2 : 1;
-      p.least = 16;
+      p.least = 32;
     }
     if (p.splits > 1) p.prompt_bytes = (size_t)(all * p.splits * 128 * (D + 2) * 4 + 255) & ~(size_t)255;
   }

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.serve_util import DTYPES, Cache, gpu, starts
+from oracle import serve
+from tests.serve_util import DTYPES, Cache, attention_bounds, f64, gpu, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,18 @@ def test_a_scale_of_zero_is_a_product_like_any_other(rows, lens, kind):
     bad[0, 1] = bad[-1, 2] = True
     assert torch.isnan(y.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
     assert torch.equal(y.cpu()[~bad], want.cpu()[~bad]) and torch.equal(lse.cpu()[~bad], want_l.cpu()[~bad])
+
+
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (128, 4200), (256, 0)])
+def test_long_chunks_of_many_heads(D, window):
+    """Blocks for more than half of the compute units, long enough to be cut in two. All heads hold the same: the first
+    is checked, the others have to be equal to it."""
+    H, rows, lens = 40, [500], [4700]
+    c = Cache(D, lens, 1, D, 64)
+    q = torch.from_numpy(np.random.default_rng(D + 1).standard_normal((500, 1, D))).bfloat16()
+    dev = [gpu(a) for a in (c.lens, c.table)] + [gpu(a).expand(-1, H, *a.shape[2:]).contiguous() for a in (c.kc, c.vc, c.ks, c.vs)]
+    y, lse = L.bsq_attention_kv8(q.cuda().repeat(1, H, 1), gpu(starts(rows)), *dev, 500, window=window)
+    ref, rl, parts = serve.attention(f64(q), starts(rows), c.lens, *c.host(), D ** -0.5, window)
+    ty, tl = attention_bounds(ref, rl, parts, q.dtype, D)
+    assert np.all(np.abs(f64(y[:, :1]) - ref) <= ty) and np.all(np.abs(f64(lse[:, :1]) - rl) <= tl)
+    assert torch.equal(y, y[:, :1].repeat(1, H, 1)) and torch.equal(lse, lse[:, :1].repeat(1, H))
