@@ -9,9 +9,14 @@
 // fp32 before its scale is applied.
 //
 // The floor is memory: K / 2 bytes a row and its scales (cold: 1 x 16384 x 8192 18.9 us, 3.9 TB/s; 1 x 4096 x 4096
-// 5.2 us, of which a launch is 3). With more tokens vector instructions bound it, some twelve for eight codes and
-// as many for each 8 x 16 values of x (24 x 12288 x 4096 in groups of 32: 26.3 us, the vector units 40 % busy, as
-// far as two waves a SIMD take them).
+// 5.2 us, of which a launch is 3). With more tokens the compute units are half empty: what a workgroup stages takes 90 KB
+// of LDS (two tiles of 32 rows and tokens to each of eight waves), so that one fits a unit, two waves a SIMD, which keep
+// the vector units 40 % busy, and the last round of workgroups fills what it fills (24 x 12288 x 4096 in groups of 32: 24 us,
+// 384 workgroups of 32 rows on 256 units).
+//
+// From 33 tokens on, two tiles of 16 rows and four of 16 tokens need more than a wave's 256 registers: 6 to 9 are
+// spilled, in groups of 32 19 (fp16) and 83 (bf16); with one tile of rows none, or 3 (48 x 8192 x 8192: 39.4 us with
+// two and 48.9 with one).
 #include <type_traits>
 
 #include "bsq_launch.hpp"

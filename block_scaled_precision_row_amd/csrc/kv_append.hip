@@ -11,7 +11,7 @@
 // Bound by memory for prompts (2 bytes read and 1 written per element, the queries twice 2): 9000 tokens of 32 + 2 x 8
 // heads of 128 in pages of 16, 214 MB, in 56 us, 3.8 TB/s (50 with angles and products in 32 bits, which
 // put three times as many keys on the wrong side); and by the chain of dependent loads (row, length, page, scale,
-// values) for a decode step: 96 tokens in 10.7 us. What counted for the prompt: one wave to a token's queries with its
+// values) for a decode step: 96 tokens in 11 us (12.2 on average). What counted for the prompt: one wave to a token's queries with its
 // loads on their way before the search for its sequence (-9 us), and the registers of a thread.
 #include "serve_device.hpp"
 
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(Args a) {
 template <class E, int D, bool INTER>
 void launch_keep(const Args& a, unsigned blocks, hipStream_t s) {
   // a page of at most 256 units needs one kept; two are worth their registers above (64 tokens of 128 elements, 9000
-  // tokens in all: 44.7 us with two, 47.8 with one; pages of 16: 44.7 and 41.2)
+  // tokens in all: 56 us with two, 62 with one; pages of 16, which never have a second: 56 with either)
   if (D / 16 << a.c.shift <= 256)
     hipLaunchKernelGGL((kv_append_kernel<E, D, INTER, 1>), dim3(blocks), dim3(256), 0, s, a);
   else

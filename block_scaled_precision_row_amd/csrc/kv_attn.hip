@@ -12,8 +12,8 @@
 //
 // Bound by memory: 2 D bytes per token and kv head. Every wave streams tiles of 64 tokens of its own
 // through two LDS buffers (16 KB each for D 128), the next tile in flight while it works on one; two
-// workgroups of 64 KB to a compute unit: 64 sequences of 4000 to 8000 tokens, 32 / 8 heads of 128, 773 MB in
-// 152 us, 5.1 TB/s, and 7 for the join. Loading the operands straight into registers, neighbouring lanes on
+// workgroups of 64 KB to a compute unit: 64 sequences of 4000 to 8000 tokens, 32 / 8 heads of 128, 773 MB, 158 us a call
+// with the join (7.5), 5.1 TB/s. Loading the operands straight into registers, neighbouring lanes on
 // neighbouring rows, left the address unit with 16-byte pieces (205 us).
 #include "kv_attn.hpp"
 
@@ -495,10 +495,12 @@ hipError_t launch_attention(bsq_dtype dt, const AttnArgs& p, void* workspace, hi
   a.max_q_len = (int)(p.max_q_len < p.T ? p.max_q_len : p.T);
   Cut plan = cut_of(p.c.batch, p.T, p.max_q_len, a.group, p.c.heads, p.c.dim);
   // Short sequences go along with the prompt kernel where none of its workgroups can have more than 64 tiles for
-  // that (one token's block costs it about what it costs the step kernel, and an idle step kernel and its join
-  // 5 to 15 us: 64 rows and 27 x 1 over 700 tokens 54 us with the step kernel, 36 without; 64 and 99 x 1 over 8000, one
-  // kv head, 124 and 96; 200 and 63 x 1 over 3000 98 and 108). A longer one would keep its workgroup for itself: 2048 rows
-  // and 7 x 1 over 8000 tokens 116 us with the step kernel, 242 without; with one of 60000 tokens 124 and 1689.
+  // that (one token's block costs it about what it costs the step kernel, and an idle step kernel and its join 3 to 4 us,
+  // 9 on the card: 64 rows and 27 x 1 over 700 tokens 43 us with the step kernel, 23 without; 64 and 99 x 1 over 8000,
+  // one kv head, 165 and 117; 200 and 63 x 1 over 3000 91 and 77). A longer one would keep its workgroup for itself: 2048 rows
+  // and 7 x 1 over 8000 tokens 112 us with the step kernel, 216 without; 2048 rows and three of 40000 to 60000 tokens 146 and
+  // 1479. That goes by the table's width, for the lengths are on the device: with a wide table the step kernel and its
+  // join are launched beside any prompt of several sequences.
   const int64_t most_tiles = ((int64_t)p.c.max_pages << p.c.shift) / kv::kTile + 1;
   if (plan.prompt && most_tiles <= 64 * (int64_t)plan.splits) plan.step = false;
   // no parts, no join, where the table has no room for a block of several (a join costs 5 us)

@@ -107,7 +107,7 @@ constexpr int tile_loads(int D) { return D / 8; }    // of 1 KB
 // 16 bytes a lane from `p` to LDS at `lds` + 16 lane. Inline assembly, so that the compiler does not
 // make every LDS read wait for it; callers wait (wait_loads) before they read. (One wait state
 // between the write of M0 and its use.) `once`: codes that nobody reads again, with the non-temporal hint (64
-// sequences of 4000 to 8000 tokens, 773 MB: 146 us with it, 158 without).
+// sequences of 4000 to 8000 tokens, 773 MB: 158 us a call with it, 166 without).
 template <bool once>
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
   if constexpr (once) asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "{m0}"(lds) : "memory");

@@ -3,7 +3,7 @@
 // Bound by memory: every element is read and written once; an angle costs some 55 instructions
 // and serves all heads of its token, so a workgroup first puts the cosines and sines of its tokens
 // into LDS and then streams the tokens' heads, 16 elements (eight pairs) a thread and step. 8192 tokens of
-// 40 heads of 128, fp16: 168 MB in 32.8 us, 5.1 TB/s, what a copy reaches; 96 tokens of 32 heads 3.1 us, a launch.
+// 40 heads of 128, fp16: 168 MB in 32.8 us, 5.1 TB/s, what a copy reaches; 48 tokens of 40 heads 3.1 us, a launch.
 #include "serve_device.hpp"
 
 namespace bsq {

@@ -38,7 +38,11 @@ typedef enum { BSQ_ROPE_HALF = 1, BSQ_ROPE_INTERLEAVED = 2 } bsq_rope_layout;
  *                    g_i = clamp((t_i - beta_slow) / (beta_fast - beta_slow), 0, 1)
  *                    and t_i = trained_len * w_i / (2 pi) is how often pair i
  *                    turns over the trained length: pairs of many turns keep
- *                    their frequency. *attn_factor = 0.1 ln(factor) + 1
+ *                    their frequency. *attn_factor = 0.1 ln(factor) + 1.
+ *                    (A ramp along the pair's index i between the pairs of
+ *                    beta_fast and beta_slow turns is another one: a checkpoint
+ *                    that was trained with it needs its own frequencies, which
+ *                    bsq_rope and bsq_kv_append take as they take these.)
  * Computed in 64 bits and rounded once to fp32. *attn_factor is 1 otherwise.
  * trained_len, beta_fast, beta_slow are read for YARN only.
  * BSQ_ERR_SHAPE: rot_dim odd, < 2 or > 1024 (for NTK also 2). BSQ_ERR_ARG: an
@@ -65,8 +69,8 @@ bsq_status bsq_rope_inv_freq(int64_t rot_dim, double base, bsq_rope_scaling scal
  *     same strides (in place), otherwise they must not overlap.
  *   positions [T] int64 (any value of magnitude below 2^53), inv_freq
  *     [rot_dim / 2] fp32
- * 1 <= D <= 1024, rot_dim even, 2 <= rot_dim <= D; T, H >= 0 (0: nothing to
- * do); strides >= 0 and < 2^40, y's rows must not overlap one another
+ * 1 <= D <= 1024, rot_dim even, 2 <= rot_dim <= D; 0 <= T <= 2^30, 0 <= H <=
+ * 65535 (0: nothing to do); strides >= 0 and < 2^40, y's rows must not overlap one another
  * (BSQ_ERR_SHAPE). Pointers aligned to their element size. BSQ_ERR_ARG for an
  * unknown dtype, layout or flag, or an attn_factor that is not finite.
  */
@@ -95,7 +99,7 @@ bsq_status bsq_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t 
  * (< 2^40), max_pages * page_size < 2^31 - 1024. k and v 16-byte aligned, the
  * others 4-byte. 0 <= T <= 2^30 and at most 65535 query heads; a call whose
  * work does not fit one launch is refused (BSQ_ERR_SHAPE): append from
- * (T / page_size + 2 batch) * kv_heads + T = 2^23 on, attention from
+ * (T / page_size + 2 batch) * kv_heads = 2^23 on (+ T with queries), attention from
  * (T * q_heads / kv_heads / 128 + batch) * kv_heads = 2^23 or
  * batch * (max_pages * page_size / 64 + 1) = 2^31 on.
  *
@@ -130,7 +134,7 @@ typedef struct {
  *   codes already there become E4M3(value * scale before / scale) (exact
  *     except where they fall below E4M3's normal range), the new ones
  *     E4M3(value / scale), rounded to nearest even, saturating at +-448.
- * NaN stays NaN and infinities saturate. Appending again with the same
+ * NaN stays NaN and infinities saturate (at 0 where the page's scale is 0). Appending again with the same
  * arguments changes nothing. Codes behind the last token are left as they are.
  *   k, v [T][kv_heads][head_dim], q, q_out [T][q_heads][head_dim] of `dtype`
  *     (BSQ_BF16 or BSQ_FP16): 16-byte aligned, strides in elements, multiples
