@@ -151,13 +151,14 @@ struct Pages {
     v_hi = (uint32_t)(v >> 32);
   }
   // Makes `vs` of the scale that load() brought (apart, so that the tile's loads need not wait for it). A page of zeros
-  // may have any exponent: a low one, so that it does not outweigh others, but not so low that its tokens leave
-  // the sum.
+  // may have any exponent: the reference's while there is none, and then a low one, so that it does not outweigh small values
+  // in rows that do not see the page that set the reference, but not so low that its tokens leave the sum or that
+  // sum, times 2^90, fp32.
   __device__ __forceinline__ void settle() {
     int e = vs >> 23 & 0xFF;
     e = absent || e == 0xFF ? 0 : e;
     if (ref == 0) ref = __builtin_amdgcn_readfirstlane((int)wave_max((float)e));
-    vs = e == 0 ? -40 : e - ref;
+    vs = e == 0 ? (ref == 0 ? 0 : -90) : e - ref;
   }
   static __device__ __forceinline__ int place(int tile, int gran) { return (tile & 15) * 4 + gran; }
   __device__ __forceinline__ int gone(int tile, int gran) const { return __shfl(absent, place(tile, gran), 64); }

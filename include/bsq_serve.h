@@ -167,7 +167,7 @@ bsq_status bsq_kv_append(bsq_dtype dtype, const bsq_kv8_cache* cache, const int3
  * second product as they are, and each token's weight, its probability times its
  * page's scale, as the sum of two fp16 numbers with an exponent of the row's own:
  * 21 bits, fewer where that would be below 2^-35 of the row's largest weight.
- * (The V scales of pages that one row sees may be up to 2^100 apart.)
+ * (The V scales of pages that one call sees may be up to 2^90 apart.)
  *   q, y [T][q_heads][head_dim] of `dtype` (BSQ_BF16 or BSQ_FP16): 16-byte
  *     aligned, strides multiples of 8 (0 <= stride < 2^40), y's rows must not
  *     overlap; lse [T][q_heads] fp32 or NULL

@@ -8,7 +8,7 @@ row is at least half of; weights are at most 2^15 and the largest is above 2^10.
 which for parts below fp16's normal range is 2^-25, at most 2^-35 of the largest weight W, so 2^-35 W sum |code| / sum p;
 by the scores, (D + 4) 2^-24 max sum |q k| scale, in numerator and denominator alike; 2^-20 for exp2 and its argument; n
 2^-24 for the sums. lse errs by the scores, n 2^-24, 2^-20, and a rounding of N and of the log of the sum, which cancel where
-scales of pages are 2^s apart: 2^-23 (|lse| + s).
+scales of pages are 2^s apart: 2^-23 (|lse| + s); a page of zeros stands at 2^-90.
 """
 import numpy as np
 import pytest
@@ -67,7 +67,7 @@ def reference(c, cu, q, scale, window=0):
                     w = e * s[m]
                     ty[r] = 1.01 * rel * (w @ np.abs(codes[m])) / e.sum() + 2.0 ** -35 * w.max() * np.abs(codes[m]).sum(0) / e.sum()
                     far = np.ptp(np.log2(s[m][s[m] > 0])) if (s[m] > 0).any() else 0.0
-                    tl[r] = score + m.sum() * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * (abs(lse[r]) + far + 50.0 * (s[m] == 0).any())
+                    tl[r] = score + m.sum() * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * (abs(lse[r]) + far + 90.0 * (s[m] == 0).any())
     return y, lse, ty, tl, seen_by
 
 
@@ -167,6 +167,19 @@ def test_pages_of_scales_far_apart(rows, lens, window, kind, lo, hi):
         c.vs[at], c.vc[at] = 2.0 ** (hi - 1), c.vc[at] | 1
     y, lse = attend(c, cu, q, max(rows), softmax_scale=0.3, window=window)
     check(c, cu, q, y, lse, 0.3, window)
+
+
+@pytest.mark.parametrize("rows,lens", [([4], [150]), ([40], [150])])
+def test_small_values_and_zeros_below_a_page_that_few_rows_see(rows, lens):
+    """Zeros and values of 2^-70 for most rows; the last sees 2^20 as well, which sets the reference of them all."""
+    c, cu, q = Cache(79, lens, 1, 64, 16), starts(rows), queries(80, rows[0], 4, 64, "bf16", 0.1)
+    c.vs[:] = 2.0 ** -70
+    zeros = c.table[0, 1:9:2]
+    c.vs[zeros], c.vc[zeros] = 0.0, 0
+    c.lens[0] = 145                                  # one token on the last page
+    c.vs[c.table[0, 9]] = 2.0 ** 20
+    y, lse = attend(c, cu, q, rows[0], softmax_scale=0.3)
+    check(c, cu, q, y, lse, 0.3)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
