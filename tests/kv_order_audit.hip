@@ -147,7 +147,7 @@ int main() {
     const int groups[] = {1, 2, 3, 4, 7, 8, 16, 20, 33, 128, 300};
     check(c, cu, T, groups[pick(0, c.batch > 9 ? 4 : 10)], pick(0, 1) ? 16 : 0, pick(0, 2) ? 0x7FFFFFFF : pick(1, 200), rising);
   }
-  // the case that a reader found: block 31 of group 4 lies before its sequence's first
+  // block 31 of group 4 lies before the first of the sequence that the search ends at
   {
     Cache c{};
     std::vector<int32_t> cu = {0, 1000, 1200, 100, 150}, lens = {2000, 1500, 300, 400}, table(4 * 40, 0);
