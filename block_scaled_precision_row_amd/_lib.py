@@ -36,6 +36,11 @@ BSQ_ROPE_PLAIN, BSQ_ROPE_LINEAR, BSQ_ROPE_NTK, BSQ_ROPE_YARN = 0, 1, 2, 3
 BSQ_ROPE_BACKWARD = 0x1
 BSQ_ATTN_FULL = 0x1
 
+# include/bsq_block.h
+BSQ_AXES_BLOCKS, BSQ_AXES_CYCLED = 1, 2
+BSQ_NORM_NONE, BSQ_NORM_LAYER, BSQ_NORM_RMS = 0, 1, 2
+BSQ_ACT_NONE, BSQ_ACT_SILU, BSQ_ACT_GELU_TANH, BSQ_ACT_GELU = 0, 1, 2, 3
+
 
 class GemmProblem(ctypes.Structure):
     """bsq_gemm_problem: one linear of a grouped launch (device pointers as integers)."""
@@ -56,7 +61,21 @@ class Kv8Cache(ctypes.Structure):
                 ("max_pages", _i64), ("table_stride", _i64)]
 
 
-# symbol -> (restype, argtypes); mirrors include/bsq.h and include/bsq_serve.h
+class Block(ctypes.Structure):
+    """bsq_block: the norms, vectors and row groups between two blocks (device pointers as integers)."""
+    _fields_ = [("dtype", _int), ("norm", _int), ("post", _int), ("eps", _f32), ("post_eps", _f32), ("rows", _i64),
+                ("dim", _i64), ("groups", _i64), ("group_starts", _p), ("weight", _p), ("bias", _p),
+                ("post_weight", _p), ("scale", _p), ("shift", _p), ("gate", _p), ("scale_stride", _i64),
+                ("shift_stride", _i64), ("gate_stride", _i64)]
+
+
+class Epilogue(ctypes.Structure):
+    """bsq_epilogue: what a linear does with its sums before they are rounded (device pointers as integers)."""
+    _fields_ = [("act", _int), ("bias", _p), ("gate", _p), ("gate_stride", _i64), ("residual", _p),
+                ("residual_stride", _i64), ("groups", _i64), ("group_starts", _p)]
+
+
+# symbol -> (restype, argtypes); mirrors include/bsq.h, include/bsq_serve.h and include/bsq_block.h
 SIGNATURES = {
     "bsq_abi_version": (_int, []),
     "bsq_status_string": (ctypes.c_char_p, [_int]),
@@ -100,6 +119,14 @@ SIGNATURES = {
     "bsq_attention_kv8": (_int, [_int, ctypes.POINTER(Kv8Cache), _p, _i64, _i64, _p, _i64, _i64, _i64, _f32, _i64,
                                  _u32, _p, _i64, _i64, _p, _p, _sz, _p]),
     "bsq_gemm_int4g": (_int, [_int, _p, _i64, _p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _p]),
+    "bsq_rope_axes": (_int, [_int, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _int, _p, _int, _f32, _u32, _p, _i64, _i64,
+                             _i64, _i64, _i64, _p]),
+    "bsq_block_norm": (_int, [ctypes.POINTER(Block), _p, _i64, _p, _i64, _p, _i64, _int, _p, _p, _i64, _p, _p]),
+    "bsq_block_norm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bsq_block_norm_backward": (_int, [ctypes.POINTER(Block)] + [_p, _i64] * 6 + [_p] * 6 + [_p, _sz, _p]),
+    "bsq_gemm_fp8r_q_epilogue": (_int, [_p, _p, _p, _p, ctypes.POINTER(Epilogue), _p, _i64, _i64, _i64, _i64, _p]),
+    "bsq_gemm_nvfp4_q_epilogue": (_int, [_p, _p, _p, _p, _p, _p, ctypes.POINTER(Epilogue), _p, _i64, _i64, _i64, _i64,
+                                         _p]),
 }
 
 
@@ -773,4 +800,209 @@ def bsq_gemm_int4g(x, w, w_scale, w_zero=None, y=None):
     _like(y, (M, N), x.dtype, dev, "y")
     _, _, ldy = _rows(y, x.dtype, "y")
     _call("bsq_gemm_int4g", dev, _DTYPES[x.dtype], x.data_ptr(), ldx, wp, sp, zp, K // groups, y.data_ptr(), ldy, M, N, K)
+    return y
+
+
+# ---- around the linears of a transformer block (include/bsq_block.h) ---------------
+# These too run on the device of their tensors, on that device's current stream.
+
+def bsq_rope_axes(x, positions, inv_freq, sections, order=BSQ_AXES_BLOCKS, layout=BSQ_ROPE_HALF, attn_factor=1.0,
+                  backward=False, y=None):
+    """bsq_rope with several axes: positions int64 [T, axes] (any strides), sections: the pairs of each axis, taken in
+    blocks or in turn (`order`); inv_freq fp32 [sum(sections)]. y may be x (in place)."""
+    shape, xt, xh = _heads(x, _DTYPES, "x")
+    T, H, D = shape
+    dev, dtype = x.device, x.dtype
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        yt, yh = (H * D if T > 1 else 0), (D if H > 1 else 0)
+    else:
+        yt, yh = _heads_like(y, shape, dtype, dev, "y")
+    axes = len(sections)
+    _like(positions, (T, axes), torch.int64, dev, "positions")
+    pt, pa = positions.stride()
+    freq = _flat(inv_freq, (sum(sections),), torch.float32, dev, "inv_freq")
+    _call("bsq_rope_axes", dev, _DTYPES[dtype], x.data_ptr(), xt, xh, positions.data_ptr(), pt, pa,
+          (ctypes.c_int64 * axes)(*sections), axes, order, freq, layout, attn_factor,
+          BSQ_ROPE_BACKWARD if backward else 0, y.data_ptr(), yt, yh, T, H, D)
+    return y
+
+
+def _row_stride(x, shape, dtype, device, name):
+    """(address, row stride) of a [rows, dim] tensor of this shape; (None, 0) for None."""
+    if x is None:
+        return None, 0
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device.index:
+        _like(x, shape, dtype, device, name)
+    st, sd = x.stride()
+    if sd != 1 and shape[1] > 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return x.data_ptr(), (st if shape[0] > 1 else 0)
+
+
+def _group_count(vectors, starts):
+    """The number of row groups, from their vectors or from where they start."""
+    for v in vectors:
+        if v is not None:
+            if v.dim() != 2:
+                raise ValueError("scale, shift and gate must be 2-D, a row for each group")
+            return v.shape[0]
+    return 1 if starts is None else starts.shape[0] - 1
+
+
+def _starts_of(starts, groups, device):
+    return None if starts is None else _flat(starts, (groups + 1,), torch.int32, device, "starts")
+
+
+def _block(x, norm, eps, weight, bias, scale, shift, gate, post, post_weight, post_eps, starts):
+    """The descriptor of a block's norms for rows like x: (Block, its shape)."""
+    if x is None or x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda:
+        raise ValueError("rows must be 2-D tensors of bfloat16, float16 or float32 on the GPU")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    rows, dim = shape
+    groups = _group_count((scale, shift, gate), starts)
+    w, b, pw = (None if v is None else _flat(v, (dim,), dtype, dev, name)
+                for v, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight")))
+    like = (groups, dim)
+    sc, scs = _row_stride(scale, like, dtype, dev, "scale")
+    sh, shs = _row_stride(shift, like, dtype, dev, "shift")
+    ga, gas = _row_stride(gate, like, dtype, dev, "gate")
+    return Block(_DTYPES[dtype], norm, post, eps, eps if post_eps is None else post_eps, rows, dim, groups,
+                 _starts_of(starts, groups, dev), w, b, pw, sc, sh, ga, scs, shs, gas)
+
+
+def bsq_block_norm(x, norm=BSQ_NORM_RMS, eps=1e-6, weight=None, bias=None, scale=None, shift=None, branch=None,
+                   gate=None, post=BSQ_NORM_NONE, post_weight=None, starts=None, post_eps=None, out_format=None,
+                   y_global=None, y=None, y_scale=None, x_out=None):
+    """x_out = x + gate * (post_weight * N_post(branch)), y = (N_norm(x_out) * weight + bias) * (1 + scale) + shift for
+    rows x, branch [T, D] (bf16, fp16 or fp32); weight, bias, post_weight [D]; scale, shift, gate [groups, D], a row for
+    each group of x's rows: starts int32 [groups + 1], or equal groups where None. out_format BSQ_FMT_FP8R or
+    BSQ_FMT_NVFP4 (with y_global [1]) encodes y for a quantized linear. Returns (y, y_scale, x_out): y_scale None
+    without an encoding, x_out None without a branch (x is then x_out), y None for BSQ_NORM_NONE."""
+    block = _block(x, norm, eps, weight, bias, scale, shift, gate, post, post_weight, post_eps, starts)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    T, D = shape
+    xp, xs = _row_stride(x, shape, dtype, dev, "x")
+    bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
+    if branch is not None and x_out is None:
+        x_out = torch.empty(shape, dtype=dtype, device=dev)
+    op, os_ = _row_stride(x_out, shape, dtype, dev, "x_out")
+    yp = ysp = None
+    ys = 0
+    if out_format is None:
+        if norm != BSQ_NORM_NONE:
+            if y is None:
+                y = torch.empty(shape, dtype=dtype, device=dev)
+            yp, ys = _row_stride(y, shape, dtype, dev, "y")
+        elif y is not None:
+            raise ValueError("y without a norm")
+        if y_scale is not None:
+            raise ValueError("y_scale without an encoding")
+    else:
+        fp8 = out_format == BSQ_FMT_FP8R
+        code_shape, scale_shape, kind = ((T, D), (T,), torch.float32) if fp8 else ((T, D // 2), (T, D // 16), torch.uint8)
+        if y is None:
+            y = torch.empty(code_shape, dtype=torch.uint8, device=dev)
+        if y_scale is None:
+            y_scale = torch.empty(scale_shape, dtype=kind, device=dev)
+        yp = _flat(y, code_shape, torch.uint8, dev, "y")
+        ysp = _flat(y_scale, scale_shape, kind, dev, "y_scale")
+    gp = None if y_global is None else _flat(y_global, (1,), torch.float32, dev, "y_global")
+    _call("bsq_block_norm", dev, block, xp, xs, bp, bs, op, os_, out_format or 0, gp, yp, ys, ysp)
+    return y, y_scale, x_out
+
+
+def bsq_block_norm_workspace_bytes(rows, dim, groups=1):
+    return lib.bsq_block_norm_workspace_bytes(rows, dim, groups)
+
+
+def bsq_block_norm_backward(dy, dx_out, x_out, norm=BSQ_NORM_RMS, eps=1e-6, weight=None, bias=None, scale=None,
+                            shift=None, branch=None, gate=None, post=BSQ_NORM_NONE, post_weight=None, starts=None,
+                            post_eps=None, need=None, dx=None, dbranch=None, workspace=None):
+    """The gradients of bsq_block_norm for those of y (dy, None for BSQ_NORM_NONE) and of x_out (dx_out, or None), from
+    its x_out (x without a branch) and its other arguments: a dict of "x", "branch" (like x), and in fp32 "gate",
+    "scale", "shift" [groups, D], "weight", "bias", "post_weight" [D], None for what the block does not have. `need`
+    names those to compute (all where None). Without gate and post norm "branch" is "x" (one tensor)."""
+    like = dx_out if dy is None else dy
+    block = _block(like, norm, eps, weight, bias, scale, shift, gate, post, post_weight, post_eps, starts)
+    shape, dtype, dev = like.shape, like.dtype, like.device
+    T, D = shape
+    groups = block.groups
+
+    def asked(name):
+        return need is None or name in need
+
+    yp, ys = _row_stride(dy, shape, dtype, dev, "dy")
+    dp, ds = _row_stride(dx_out, shape, dtype, dev, "dx_out")
+    op, os_ = _row_stride(x_out, shape, dtype, dev, "x_out")
+    bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
+    own_branch = branch is not None and asked("branch") and (gate is not None or post != BSQ_NORM_NONE)
+    if dx is None and (asked("x") or (branch is not None and asked("branch") and not own_branch)):
+        dx = torch.empty(shape, dtype=dtype, device=dev)
+    if dbranch is None and own_branch:
+        dbranch = torch.empty(shape, dtype=dtype, device=dev)
+    xp, xs = _row_stride(dx, shape, dtype, dev, "dx")
+    hp, hs = _row_stride(dbranch, shape, dtype, dev, "dbranch")
+
+    def grad(vector, name, size):
+        return torch.empty(size, dtype=torch.float32, device=dev) if vector is not None and asked(name) else None
+
+    out = {"x": dx, "branch": dbranch if dbranch is not None or branch is None or not asked("branch") else dx,
+           "gate": grad(gate, "gate", (groups, D)), "scale": grad(scale, "scale", (groups, D)),
+           "shift": grad(shift, "shift", (groups, D)), "weight": grad(weight, "weight", (D,)),
+           "bias": grad(bias, "bias", (D,)), "post_weight": grad(post_weight, "post_weight", (D,))}
+    vectors = [None if out[k] is None else out[k].data_ptr()
+               for k in ("scale", "shift", "gate", "weight", "bias", "post_weight")]
+    if workspace is None:
+        if any(v is not None for v in vectors) and T:
+            workspace = torch.empty((lib.bsq_block_norm_workspace_bytes(T, D, groups),), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on %s" % dev)
+    _call("bsq_block_norm_backward", dev, block, yp, ys, dp, ds, op, os_, bp, bs, xp, xs, hp, hs, *vectors,
+          None if workspace is None else workspace.data_ptr(), _nbytes(workspace))
+    return out
+
+
+def _epilogue(M, N, bias, act, gate, residual, starts, y, dev):
+    """The descriptor of an epilogue, y and its leading dimension."""
+    bf16 = torch.bfloat16
+    groups = _group_count((gate,), starts)
+    bp = None if bias is None else _flat(bias, (N,), bf16, dev, "bias")
+    gp, gs = _row_stride(gate, (groups, N), bf16, dev, "gate")
+    rp, rs = _row_stride(residual, (M, N), bf16, dev, "residual")
+    if y is None:
+        y = torch.empty((M, N), dtype=bf16, device=dev)
+    yp, ys = _row_stride(y, (M, N), bf16, dev, "y")
+    return Epilogue(act, bp, gp, gs, rp, rs if M > 1 else N, groups, _starts_of(starts, groups, dev)), y, yp, (
+        ys if M > 1 else N)
+
+
+def bsq_gemm_fp8r_q_epilogue(xq, x_scale, w, w_scale, bias=None, act=BSQ_ACT_NONE, gate=None, residual=None, starts=None,
+                             y=None):
+    """bsq_gemm_fp8r_q with an epilogue: bf16 y [M, N] = residual + gate * act(linear(x) + bias), bias [N], residual
+    [M, N] (may be y), gate [groups, N] with a row for each group of rows (starts int32 [groups + 1], equal groups where
+    None), all bf16 or None."""
+    dev, (M, K), N = xq.device, xq.shape, w.shape[0]
+    xp = _flat(xq, (M, K), torch.uint8, dev, "xq")
+    sp = _flat(x_scale, (M,), torch.float32, dev, "x_scale")
+    wp = _flat(w, (N, K), torch.uint8, dev, "w")
+    wsp = _flat(w_scale, (N,), torch.float32, dev, "w_scale")
+    e, y, yp, ldy = _epilogue(M, N, bias, act, gate, residual, starts, y, dev)
+    _call("bsq_gemm_fp8r_q_epilogue", dev, xp, sp, wp, wsp, e, yp, ldy, M, N, K)
+    return y
+
+
+def bsq_gemm_nvfp4_q_epilogue(xq, x_bscale, input_scale, w, w_bscale, w_scale2, bias=None, act=BSQ_ACT_NONE, gate=None,
+                              residual=None, starts=None, y=None):
+    """bsq_gemm_nvfp4_q with an epilogue, as bsq_gemm_fp8r_q_epilogue."""
+    dev, (M, half), N = xq.device, xq.shape, w.shape[0]
+    K = 2 * half
+    xp = _flat(xq, (M, half), torch.uint8, dev, "xq")
+    sp = _flat(x_bscale, (M, K // 16), torch.uint8, dev, "x_bscale")
+    ip = _flat(input_scale, (1,), torch.float32, dev, "input_scale")
+    wp = _flat(w, (N, half), torch.uint8, dev, "w")
+    wsp = _flat(w_bscale, (N, K // 16), torch.uint8, dev, "w_bscale")
+    gp = _flat(w_scale2, (1,), torch.float32, dev, "w_scale2")
+    e, y, yp, ldy = _epilogue(M, N, bias, act, gate, residual, starts, y, dev)
+    _call("bsq_gemm_nvfp4_q_epilogue", dev, xp, sp, ip, wp, wsp, gp, e, yp, ldy, M, N, K)
     return y

@@ -12,6 +12,7 @@
 #include <string>
 #include <utility>
 
+#include "block_launch.hpp"
 #include "bsq_launch.hpp"
 #include "serve_launch.hpp"
 
@@ -358,6 +359,72 @@ bsq_status bsq_gemm_nvfp4_q(const uint8_t* xq, const uint8_t* x_bscale, const fl
   a.y = y; a.ldy = ldy; a.M = M; a.N = N; a.K = K;
   hipError_t e = launch_dec_or_skinny(bsq::kW4A4, a, stream);
   return e == hipSuccess ? BSQ_OK : hip_fail(e);
+}
+
+// ---- with an epilogue (include/bsq_block.h) ---------------------------------------------
+namespace {
+// the epilogue of an M x N linear, M and N > 0
+bsq_status check_epilogue(const bsq_epilogue* p, const uint16_t* y, int64_t ldy, int64_t M, int64_t N,
+                          bsq::Epilogue& e) {
+  if (!p) return BSQ_ERR_NULL;
+  if (p->act < BSQ_ACT_NONE || p->act > BSQ_ACT_GELU) return BSQ_ERR_ARG;
+  e = bsq::Epilogue{};
+  e.act = (int)p->act;
+  if (!aligned(p->bias, 2)) return BSQ_ERR_ALIGN;
+  e.bias = p->bias;
+  if (p->gate) {
+    if (p->groups < 1 || p->groups > (int64_t)1 << 24 || (!p->group_starts && M % p->groups != 0)) return BSQ_ERR_SHAPE;
+    if (p->gate_stride < 0 || p->gate_stride >= (int64_t)1 << 40 || (p->groups > 1 && p->gate_stride < N))
+      return BSQ_ERR_SHAPE;
+    if (!aligned(p->gate, 2) || !aligned(p->group_starts, 4)) return BSQ_ERR_ALIGN;
+    e.gate = p->gate;
+    e.gate_stride = p->gate_stride;
+    e.groups = bsq::RowGroups{p->group_starts, (int)p->groups, (int)(M / p->groups), (int)M};
+  }
+  if (p->residual) {
+    if (p->residual_stride < N || p->residual_stride >= (int64_t)1 << 40) return BSQ_ERR_SHAPE;
+    if (p->residual == y && M > 1 && p->residual_stride != ldy) return BSQ_ERR_SHAPE;
+    if (!aligned(p->residual, 16)) return BSQ_ERR_ALIGN;
+    e.residual = p->residual;
+    e.residual_stride = p->residual_stride;
+  }
+  bsq::act_coefficients(e);
+  return BSQ_OK;
+}
+}  // namespace
+
+bsq_status bsq_gemm_fp8r_q_epilogue(const uint8_t* xq, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                    const bsq_epilogue* epilogue, uint16_t* y, int64_t ldy, int64_t M, int64_t N,
+                                    int64_t K, hipStream_t stream) {
+  bsq_status st = check_fp8r_q(xq, x_scale, w, w_scale, y, ldy, M, N, K);
+  if (st != BSQ_OK || M == 0 || N == 0) return st;
+  bsq::Epilogue e;
+  if ((st = check_epilogue(epilogue, y, ldy, M, N, e)) != BSQ_OK) return st;
+  if ((st = check_device()) != BSQ_OK) return st;
+  bsq::DecArgs a{};
+  a.xq = xq; a.sx = x_scale; a.w = w; a.sw = w_scale; a.y = y; a.ldy = ldy; a.M = M; a.N = N; a.K = K;
+  const hipError_t r = route_skinny(bsq::kW8A8, a) ? bsq::launch_gemm_skinny_epilogue(bsq::kW8A8, a, e, stream)
+                                                   : bsq::launch_gemm_fp8_epilogue(a, e, stream);
+  return r == hipSuccess ? BSQ_OK : hip_fail(r);
+}
+
+bsq_status bsq_gemm_nvfp4_q_epilogue(const uint8_t* xq, const uint8_t* x_bscale, const float* input_scale,
+                                     const uint8_t* w, const uint8_t* w_bscale, const float* w_scale2,
+                                     const bsq_epilogue* epilogue, uint16_t* y, int64_t ldy, int64_t M, int64_t N,
+                                     int64_t K, hipStream_t stream) {
+  bsq_status st = check_nvfp4_q(xq, x_bscale, input_scale, w, w_bscale, w_scale2, y, ldy, M, N, K);
+  if (st != BSQ_OK || M == 0 || N == 0) return st;
+  bsq::Epilogue e;
+  if ((st = check_epilogue(epilogue, y, ldy, M, N, e)) != BSQ_OK) return st;
+  if ((st = check_device()) != BSQ_OK) return st;
+  bsq::DecArgs a{};
+  a.xq = xq; a.xs = x_bscale; a.gx = input_scale; a.w = w; a.ws = w_bscale; a.gw = w_scale2;
+  a.y = y; a.ldy = ldy; a.M = M; a.N = N; a.K = K;
+  hipError_t r;
+  if (route_skinny(bsq::kW4A4, a)) r = bsq::launch_gemm_skinny_epilogue(bsq::kW4A4, a, e, stream);
+  else if (bsq::gemm_w4a4_supported(a)) r = bsq::launch_gemm_w4a4_epilogue(a, e, stream);
+  else r = bsq::launch_gemm_dec_epilogue(a, e, stream);
+  return r == hipSuccess ? BSQ_OK : hip_fail(r);
 }
 
 static_assert(BSQ_MAX_GROUP == bsq::kMaxGroup, "the header states the group limit");

@@ -72,6 +72,27 @@ bsq_status finish(hipError_t e) { return e == hipSuccess ? BSQ_OK : bsq::hip_fai
 
 }  // namespace
 
+namespace bsq {
+bsq_status check_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t x_stride_h, const int64_t* positions,
+                      const float* inv_freq, int64_t rot_dim, bsq_rope_layout layout, float attn_factor, uint32_t flags,
+                      const void* y, int64_t y_stride_t, int64_t y_stride_h, int64_t T, int64_t H, int64_t D) {
+  if (!is16(dtype) && dtype != BSQ_FP32) return BSQ_ERR_ARG;
+  if (flags & ~BSQ_ROPE_BACKWARD) return BSQ_ERR_ARG;
+  bsq_status st = check_rotation(rot_dim, layout, attn_factor);
+  if (st != BSQ_OK) return st;
+  if (D < 1 || D > 1024 || rot_dim < 2 || rot_dim > D) return BSQ_ERR_SHAPE;
+  if (T < 0 || T > kMaxRows || H < 0 || H > 65535) return BSQ_ERR_SHAPE;
+  if (!stride_ok(x_stride_t, x_stride_h) || !stride_ok(y_stride_t, y_stride_h)) return BSQ_ERR_SHAPE;
+  if (!rows_apart(y_stride_t, y_stride_h, T, H, D)) return BSQ_ERR_SHAPE;
+  if (x == y && ((T > 1 && x_stride_t != y_stride_t) || (H > 1 && x_stride_h != y_stride_h))) return BSQ_ERR_SHAPE;
+  if (T == 0 || H == 0) return BSQ_OK;
+  if (!x || !y || !positions || !inv_freq) return BSQ_ERR_NULL;
+  const uintptr_t size = dtype == BSQ_FP32 ? 4 : 2;
+  if (!aligned(x, size) || !aligned(y, size) || !aligned(positions, 8) || !aligned(inv_freq, 4)) return BSQ_ERR_ALIGN;
+  return current_device_status();
+}
+}  // namespace bsq
+
 extern "C" {
 
 bsq_status bsq_rope_inv_freq(int64_t rot_dim, double base, bsq_rope_scaling scaling, double factor,
@@ -108,20 +129,9 @@ bsq_status bsq_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t 
                     const int64_t* positions, const float* inv_freq, int64_t rot_dim, bsq_rope_layout layout,
                     float attn_factor, uint32_t flags, void* y, int64_t y_stride_t, int64_t y_stride_h, int64_t T,
                     int64_t H, int64_t D, hipStream_t stream) {
-  if (!is16(dtype) && dtype != BSQ_FP32) return BSQ_ERR_ARG;
-  if (flags & ~BSQ_ROPE_BACKWARD) return BSQ_ERR_ARG;
-  bsq_status st = check_rotation(rot_dim, layout, attn_factor);
-  if (st != BSQ_OK) return st;
-  if (D < 1 || D > 1024 || rot_dim < 2 || rot_dim > D) return BSQ_ERR_SHAPE;
-  if (T < 0 || T > kMaxRows || H < 0 || H > 65535) return BSQ_ERR_SHAPE;
-  if (!stride_ok(x_stride_t, x_stride_h) || !stride_ok(y_stride_t, y_stride_h)) return BSQ_ERR_SHAPE;
-  if (!rows_apart(y_stride_t, y_stride_h, T, H, D)) return BSQ_ERR_SHAPE;
-  if (x == y && ((T > 1 && x_stride_t != y_stride_t) || (H > 1 && x_stride_h != y_stride_h))) return BSQ_ERR_SHAPE;
-  if (T == 0 || H == 0) return BSQ_OK;
-  if (!x || !y || !positions || !inv_freq) return BSQ_ERR_NULL;
-  const uintptr_t size = dtype == BSQ_FP32 ? 4 : 2;
-  if (!aligned(x, size) || !aligned(y, size) || !aligned(positions, 8) || !aligned(inv_freq, 4)) return BSQ_ERR_ALIGN;
-  if ((st = bsq::current_device_status()) != BSQ_OK) return st;
+  const bsq_status st = bsq::check_rope(dtype, x, x_stride_t, x_stride_h, positions, inv_freq, rot_dim, layout,
+                                        attn_factor, flags, y, y_stride_t, y_stride_h, T, H, D);
+  if (st != BSQ_OK || T == 0 || H == 0) return st;
   return finish(bsq::launch_rope(dtype, bsq::Strided{x, x_stride_t, x_stride_h}, positions,
                                  bsq::Rotation{inv_freq, (int)rot_dim, layout == BSQ_ROPE_INTERLEAVED, attn_factor},
                                  (flags & BSQ_ROPE_BACKWARD) != 0, bsq::Strided{y, y_stride_t, y_stride_h}, T, (int)H,

@@ -53,6 +53,9 @@ __device__ __forceinline__ void dma4(v4i rsrc, uint32_t lds, int voff, int soff)
   asm volatile("buffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds));
 }
 
+// a GEMM tile whose scaled sums are rounded to bf16 and stored, and nothing else
+struct NoFinish {};
+
 // ---- bf16 epilogue --------------------------------------------------------------
 // acc[i][j] is the 32x32 tile (n-tile i, m-tile j) of this wave; `scale(n)`
 // gives the per-output factor (row scales and global scales folded in by the

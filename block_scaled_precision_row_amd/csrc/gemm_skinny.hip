@@ -30,6 +30,7 @@
 // (16-bit MFMAs) or 32 (fp8 MFMA) consecutive values -- the same for both
 // operands, so every product pairs equal K indices. Workgroups start their walk over K at
 // different stages (see stage_k).
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 #include "bsq_launch.hpp"
 
@@ -203,10 +204,14 @@ __device__ __forceinline__ void skinny_lora_tile(const DecArgs& a, float* lred, 
 }
 
 // lred: the adapter tiles (LORA), added to the scaled sums: y = bf16(acc * scale + T B^T)
-template <int MODE, int MB, int NW, bool LORA>
+// Finish: what becomes of the scaled sums (ValueEpilogue of epilogue.hpp); NoFinish: y is their bf16.
+template <int MODE, int MB, int NW, bool LORA, class Finish>
 __device__ __forceinline__ void skinny_epilogue(const DecArgs& a, const float* red, const float* lred, int m0, int n0,
-                                                int tid) {
-  const int M = (int)a.M, N = (int)a.N;
+                                                int tid, const Finish& finish) {
+  constexpr bool kFinish = !std::is_same<Finish, NoFinish>::value;
+  int M = (int)a.M;
+  const int N = (int)a.N;
+  if constexpr (kFinish) M = finish.rows(M);
   float alpha = 1.0f;
   if constexpr (MODE == kW4A4) alpha = a.gx[0] * a.gw[0];
   if constexpr (MODE == kW4A16) alpha = a.gw[0];
@@ -243,10 +248,16 @@ __device__ __forceinline__ void skinny_epilogue(const DecArgs& a, const float* r
       y0 += lv[0];
       y1 += lv[1];
     }
+    if constexpr (kFinish) {
+      if (n < N) finish.pair(y0, y1, m, n, n + 1 < N);
+    }
     const uint32_t pk = pack_bf16x2(y0, y1);
     uint16_t* yr = a.y + (int64_t)m * a.ldy;
-    if (n + 1 < N) {
+    if (n + 1 < N && (!kFinish || (a.ldy & 1) == 0)) {
       *reinterpret_cast<uint32_t*>(yr + n) = pk;
+    } else if (n + 1 < N) {
+      yr[n] = (uint16_t)(pk & 0xFFFFu);
+      yr[n + 1] = (uint16_t)(pk >> 16);
     } else if (n < N) {
       yr[n] = (uint16_t)(pk & 0xFFFFu);
     }
@@ -370,8 +381,8 @@ __device__ __forceinline__ void read_bf16(OpBf& o, const uint8_t* codes, int lr,
 }
 
 // One workgroup's 32 weight rows and MB activation blocks: workgroup `bid` of the grid.
-template <int MODE, int MB, bool LORA, int NWV>
-__device__ __forceinline__ void skinny_staged_tile(const DecArgs& a, int bid) {
+template <int MODE, int MB, bool LORA, int NWV, class Finish = NoFinish>
+__device__ __forceinline__ void skinny_staged_tile(const DecArgs& a, int bid, const Finish& finish = Finish{}) {
   static_assert(MODE == kW4A4 || MODE == kW4A16, "nvfp4 weights only");
   using S = Scheme<MODE>;
   constexpr int NW = NWV;
@@ -482,7 +493,7 @@ __device__ __forceinline__ void skinny_staged_tile(const DecArgs& a, int bid) {
     for (int r = 0; r < 16; ++r) red[((wave * MB + j) * 16 + r) * 64 + lane] = acc[j][r];
   if constexpr (LORA) skinny_lora_tile<MB>(a, lred, m0, n0, wave, lane);
   __syncthreads();
-  skinny_epilogue<MODE, MB, NW, LORA>(a, red, lred, m0, n0, tid);
+  skinny_epilogue<MODE, MB, NW, LORA>(a, red, lred, m0, n0, tid, finish);
 }
 
 template <int MODE, int MB, bool LORA, int NWV = kSkStagedWaves>
@@ -541,8 +552,8 @@ __device__ __forceinline__ void read_bf(OpBf& o, const uint8_t* codes, int lr, i
 }
 
 // One workgroup's 32 weight rows and MB activation blocks: workgroup `bid` of the grid.
-template <int MODE, int MB, int NW, bool LORA>
-__device__ __forceinline__ void skinny_tile(const DecArgs& a, int bid) {
+template <int MODE, int MB, int NW, bool LORA, class Finish = NoFinish>
+__device__ __forceinline__ void skinny_tile(const DecArgs& a, int bid, const Finish& finish = Finish{}) {
   using S = Scheme<MODE>;
   using L = Layout<MODE>;
   using SC = SkCfg<MODE, MB, NW, LORA>;
@@ -632,7 +643,7 @@ __device__ __forceinline__ void skinny_tile(const DecArgs& a, int bid) {
   if constexpr (LORA) skinny_lora_tile<MB>(a, lred, m0, n0, wave, lane);
   __syncthreads();
 
-  skinny_epilogue<MODE, MB, NW, LORA>(a, red, lred, m0, n0, tid);
+  skinny_epilogue<MODE, MB, NW, LORA>(a, red, lred, m0, n0, tid, finish);
 }
 
 template <int MODE, int MB, int NW, bool LORA>
@@ -660,9 +671,27 @@ __global__ __launch_bounds__(64 * NW) void gemm_skinny_grouped_kernel(SkGroup g)
   skinny_tile<MODE, MB, NW, false>(g.p[p], bid - g.start[p]);
 }
 
+// with an epilogue on the sums (no adapter, no quantized output)
+template <int MODE, int MB, int NWV, int ACT>
+__global__ __launch_bounds__(64 * NWV) void gemm_skinny_staged_epilogue_kernel(DecArgs a, ValueEpilogue<ACT> e) {
+  skinny_staged_tile<MODE, MB, false, NWV>(a, blockIdx.x, e);
+}
+template <int MODE, int MB, int NW, int ACT>
+__global__ __launch_bounds__(64 * NW) void gemm_skinny_epilogue_kernel(DecArgs a, ValueEpilogue<ACT> e) {
+  skinny_tile<MODE, MB, NW, false>(a, blockIdx.x, e);
+}
+
 template <int MODE, int MB, int NW>
-hipError_t run(const DecArgs& a, hipStream_t s) {
+hipError_t run(const DecArgs& a, const Epilogue* ep, hipStream_t s) {
   const int64_t blocks = ((a.N + 31) / 32) * ((a.M + 32 * MB - 1) / (32 * MB));
+  if constexpr (MODE == kW8A8) {
+    if (ep)
+      return with_kind<ValueEpilogue>(*ep, [&](auto e) {
+        hipLaunchKernelGGL((gemm_skinny_epilogue_kernel<MODE, MB, NW, decltype(e)::act>), dim3((unsigned)blocks),
+                           dim3(64 * NW), 0, s, a, e);
+        return hipGetLastError();
+      });
+  }
   if (a.lt)
     hipLaunchKernelGGL((gemm_skinny_kernel<MODE, MB, NW, true>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, a);
   else
@@ -670,8 +699,16 @@ hipError_t run(const DecArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 template <int MODE, int MB, int NW = kSkStagedWaves>
-hipError_t run_staged(const DecArgs& a, hipStream_t s) {
+hipError_t run_staged(const DecArgs& a, const Epilogue* ep, hipStream_t s) {
   const int64_t blocks = ((a.N + 31) / 32) * ((a.M + 32 * MB - 1) / (32 * MB));
+  if constexpr (MODE == kW4A4) {
+    if (ep)
+      return with_kind<ValueEpilogue>(*ep, [&](auto e) {
+        hipLaunchKernelGGL((gemm_skinny_staged_epilogue_kernel<MODE, MB, NW, decltype(e)::act>),
+                           dim3((unsigned)blocks), dim3(64 * NW), 0, s, a, e);
+        return hipGetLastError();
+      });
+  }
   if (a.lt)
     hipLaunchKernelGGL((gemm_skinny_staged_kernel<MODE, MB, true, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s,
                        a);
@@ -682,7 +719,7 @@ hipError_t run_staged(const DecArgs& a, hipStream_t s) {
 }
 
 template <int MODE>
-hipError_t pick(const DecArgs& a, hipStream_t s) {
+hipError_t pick(const DecArgs& a, const Epilogue* ep, hipStream_t s) {
   // One 32-token activation block per workgroup while two per workgroup would leave the grid
   // short of the 256 compute units (measured with cold weights, K = 3072, N = 3072: W4A4 48 and
   // 64 tokens 15.9 / 16.7 -> 9.4 / 11.1 us, W8A8 48 / 64 / 96 / 128 tokens 9.1 / 9.8 / 9.2 / 9.9
@@ -695,26 +732,26 @@ hipError_t pick(const DecArgs& a, hipStream_t s) {
     // K = 3072, N = 12288: 16 / 32 / 64 tokens 12.7 / 15.8 / 20.5 -> 12.3 / 14.5 / 19.3 us; at
     // N = 3072 (96 workgroups) and for a single token eight stay ahead (8.0 vs 8.5, 10.7 vs 11.3).
     if (a.M <= 64) {
-      if (a.M >= 16 && (a.N + 31) / 32 >= 256) return run_staged<MODE, 1, 4>(a, s);
-      return run_staged<MODE, 1>(a, s);
+      if (a.M >= 16 && (a.N + 31) / 32 >= 256) return run_staged<MODE, 1, 4>(a, ep, s);
+      return run_staged<MODE, 1>(a, ep, s);
     }
-    return run_staged<MODE, 2>(a, s);
+    return run_staged<MODE, 2>(a, ep, s);
   } else if constexpr (MODE == kW4A16) {
     // bf16 activations fill registers and LDS fastest: one activation block per workgroup; on a
     // full grid four waves (N = 12288: 1 / 16 / 32 tokens 14.4 / 17.4 / 21.1 -> 13.0 / 14.8 /
     // 17.4 us; at N = 3072 eight stay ahead, 9.2 vs 10.4 at 16 tokens)
-    if ((a.N + 31) / 32 >= 256) return run_staged<MODE, 1, 4>(a, s);
-    return run_staged<MODE, 1>(a, s);
+    if ((a.N + 31) / 32 >= 256) return run_staged<MODE, 1, 4>(a, ep, s);
+    return run_staged<MODE, 1>(a, ep, s);
   } else if constexpr (MODE == kW8A16) {
     // two waves per workgroup once the grid fills the compute units (cold weights, K = 3072,
     // N = 12288, 1 / 16 tokens: 12.7 / 14.2 -> 11.8 / 13.4 us; at N = 3072 four stay ahead)
-    if (a.M <= 16 && (a.N + 31) / 32 >= 256) return run<MODE, 1, 2>(a, s);
-    return run<MODE, 1, 4>(a, s);
+    if (a.M <= 16 && (a.N + 31) / 32 >= 256) return run<MODE, 1, 2>(a, ep, s);
+    return run<MODE, 1, 4>(a, ep, s);
   } else {
     // eight waves for a handful of tokens on a small grid (1 x 3072 x 3072: 6.1 -> 5.5 us)
-    if (a.M <= 8 && short_grid) return run<MODE, 1, 8>(a, s);
-    if (a.M <= 32 || short_grid) return run<MODE, 1, 4>(a, s);
-    return run<MODE, 2, 4>(a, s);
+    if (a.M <= 8 && short_grid) return run<MODE, 1, 8>(a, ep, s);
+    if (a.M <= 32 || short_grid) return run<MODE, 1, 4>(a, ep, s);
+    return run<MODE, 2, 4>(a, ep, s);
   }
 }
 
@@ -726,12 +763,16 @@ bool gemm_skinny_supported(DecMode mode, const DecArgs& a) {
   return 64 * a.K < kOutOfRange && 64 * xpitch < (int64_t)kOutOfRange;
 }
 
+hipError_t launch_gemm_skinny_epilogue(DecMode mode, const DecArgs& a, const Epilogue& ep, hipStream_t s) {
+  return mode == kW4A4 ? pick<kW4A4>(a, &ep, s) : pick<kW8A8>(a, &ep, s);
+}
+
 hipError_t launch_gemm_skinny(DecMode mode, const DecArgs& a, hipStream_t s) {
   switch (mode) {
-    case kW4A4: return pick<kW4A4>(a, s);
-    case kW4A16: return pick<kW4A16>(a, s);
-    case kW8A8: return pick<kW8A8>(a, s);
-    default: return pick<kW8A16>(a, s);
+    case kW4A4: return pick<kW4A4>(a, nullptr, s);
+    case kW4A16: return pick<kW4A16>(a, nullptr, s);
+    case kW8A8: return pick<kW8A8>(a, nullptr, s);
+    default: return pick<kW8A16>(a, nullptr, s);
   }
 }
 

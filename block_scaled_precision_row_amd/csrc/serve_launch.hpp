@@ -27,6 +27,11 @@ struct Rotation {
   float factor;
 };
 
+// what every rotation checks (bsq_serve.cpp): its arguments and, where there is work (T > 0, H > 0), the device
+bsq_status check_rope(bsq_dtype dtype, const void* x, int64_t x_stride_t, int64_t x_stride_h, const int64_t* positions,
+                      const float* inv_freq, int64_t rot_dim, bsq_rope_layout layout, float attn_factor, uint32_t flags,
+                      const void* y, int64_t y_stride_t, int64_t y_stride_h, int64_t T, int64_t H, int64_t D);
+
 hipError_t launch_rope(bsq_dtype dt, Strided x, const int64_t* positions, Rotation r, bool backward, Strided y,
                        int64_t T, int H, int D, hipStream_t s);
 

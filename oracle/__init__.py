@@ -32,10 +32,11 @@ Modules:
   gemm    -- fp64 reference products and an exact rational dot product
   lora    -- the low-rank adapter side path, y = base + s (X A^T) B^T
   serve   -- rotary positions, the paged E4M3 cache (append, attention), 4-bit group-scaled products
+  block   -- rotary positions with several axes, gated residual and norms (and gradients), epilogues of linears
 
 Pinned functions: every public function here is checked by ``tests/`` against
 value sets, brute-force searches, closed forms, invariants or exact rational
 arithmetic (see ``tests/test_oracle_*.py``). No function is "parity unpinned".
 """
 
-from . import codec, quant, dequant, gemm, lora, serve  # noqa: F401
+from . import block, codec, quant, dequant, gemm, lora, serve  # noqa: F401

@@ -1,0 +1,186 @@
+"""GPU parity tests of the linears with an epilogue against the fp64 oracle (oracle/block.py); tolerances are derived in
+tests/block_util.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block
+from oracle.codec import e2m1_decode, e4m3_decode
+from tests.block_util import f64
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from block_scaled_precision_row_amd import _lib as L
+
+ACTS = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu": 3}
+
+
+def operands(fmt, M, N, K, seed):
+    """(the linear's operands on the GPU, the fp64 product and the sum of its terms' magnitudes)"""
+    g = torch.Generator().manual_seed(seed)
+    if fmt == "fp8r":
+        c = lambda *s: (torch.randn(*s, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+        xq, w = c(M, K), c(N, K)
+        sx, sw = torch.rand(M, generator=g) * 0.02 + 0.005, (torch.rand(N, generator=g) + 0.5) / (100 * K ** 0.5)
+        x64, w64 = (e4m3_decode(t.numpy()).astype(np.float64) for t in (xq, w))
+        x64, w64 = x64 * f64(sx)[:, None], w64 * f64(sw)[:, None]
+        args = [t.cuda() for t in (xq, sx, w, sw)]
+    else:
+        q = lambda r: torch.randint(0, 256, (r, K // 2), generator=g, dtype=torch.uint8)  # noqa: E731
+        b = lambda r: (torch.rand(r, K // 16, generator=g) * 300 + 20).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+        xq, xs, w, ws = q(M), b(M), q(N), b(N)
+        gx, gw = torch.tensor([1 / 500]), torch.tensor([1 / (500 * K ** 0.5)])
+
+        def values(c, s, g):
+            v = np.stack([e2m1_decode(c.numpy() & 15), e2m1_decode(c.numpy() >> 4)], -1).reshape(len(c), K)
+            return v * np.repeat(e4m3_decode(s.numpy()).astype(np.float64), 16, 1) * float(g)
+        x64, w64 = values(xq, xs, gx), values(w, ws, gw)
+        args = [t.cuda() for t in (xq, xs, gx, w, ws, gw)]
+    f = L.bsq_gemm_fp8r_q_epilogue if fmt == "fp8r" else L.bsq_gemm_nvfp4_q_epilogue
+    plain = L.bsq_gemm_fp8r_q if fmt == "fp8r" else L.bsq_gemm_nvfp4_q
+    return f, plain, args, x64 @ w64.T, np.abs(x64) @ np.abs(w64).T
+
+
+def bf(g, *s, size=1.0):
+    return (torch.randn(*s, generator=g) * size).bfloat16().cuda()
+
+
+def check(y, v, mag, K, bias, act, gate, residual, group):
+    """|y - ref| within the bound, for rows with a group"""
+    b = None if bias is None else f64(bias)
+    ref = block.epilogue(v, b, act, None if gate is None else f64(gate), None if residual is None else f64(residual), group)
+    e = K * 2.0 ** -24 * mag + 2.0 ** -22 * np.abs(v)
+    inner = np.abs(v) + (0.0 if b is None else np.abs(b))
+    a = block.activation(v if b is None else v + b, act)
+    e = (e + 2.0 ** -22 * inner) * (1.0 if act == "none" else 1.2)
+    if act != "none":
+        e = e + 2.0 ** -15 * np.abs(a) + (4e-7 if act == "gelu" else 0.0)
+    k = 1.0
+    if gate is not None:
+        k = block._rows(f64(gate), np.zeros(len(v), dtype=np.int64) if group is None else group, 1.0, v.shape[1])
+    e = np.abs(k) * e + 2.0 ** -22 * (np.abs(k * a) + (0.0 if residual is None else np.abs(f64(residual))))
+    live = slice(None) if group is None else group >= 0
+    bad = np.abs(f64(y) - ref)[live] - (e + 2.0 ** -8 * np.abs(ref) + 2.0 ** -100)[live]
+    assert np.all(bad <= 0), bad.max()
+
+
+# rows, columns, K (fp8r, nvfp4): few tokens, each tile, edges, K off the tiles' depth
+SHAPES = [(1, 64, 256), (2, 1000, 256), (24, 4096, 512), (33, 40, 96), (64, 2500, 288), (100, 33, 256), (128, 8192, 256),
+          (200, 72, 160), (257, 1234, 512), (300, 8000, 256), (600, 3000, 256), (1030, 2049, 288), (1500, 6000, 256),
+          (2300, 2304, 1024), (4096, 4096, 256), (4500, 6100, 256), (4200, 3840, 512)]
+
+
+@pytest.mark.parametrize("fmt", ["fp8r", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_epilogue(fmt, M, N, K):
+    f, plain, args, v, mag = operands(fmt, M, N, K, M + N)
+    g = torch.Generator().manual_seed(M)
+    bias, residual = bf(g, N), bf(g, M, N, size=2.0)
+    groups = min(M, 5)
+    cuts = np.sort(np.random.default_rng(M).integers(0, M + 1, groups))
+    starts = [0] + cuts.tolist()
+    gate = bf(g, groups, N, size=0.7)
+    group, st = block.group_of_rows(M, groups, starts), torch.tensor(starts, dtype=torch.int32).cuda()
+    # nothing asked for: the plain linear's bits, on whatever tile, since every tile sums in the same order but for the
+    # few-token kernels, which are the same here
+    assert torch.equal(f(*args), plain(*args))
+    big = M * N > 1 << 22
+    for act in ("silu",) if big else ("none", "silu", "gelu_tanh", "gelu"):
+        check(f(*args, bias=bias, act=ACTS[act]), v, mag, K, bias, act, None, None, None)
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    f(*args, bias=bias, act=ACTS["gelu"], gate=gate, residual=residual, starts=st, y=y)
+    check(y, v, mag, K, bias, "gelu", gate, residual, group)
+    assert torch.all(y[starts[-1]:] == 7.0)                      # rows behind the last group
+    # the residual in place; one group; no bias
+    mine = residual.clone()
+    assert f(*args, gate=gate[:1], residual=mine, y=mine) is mine
+    check(mine, v, mag, K, None, "none", gate[:1], residual, None)
+    check(f(*args, residual=residual, act=ACTS["gelu_tanh"]), v, mag, K, None, "gelu_tanh", None, residual, None)
+
+
+@pytest.mark.parametrize("fmt", ["fp8r", "nvfp4"])
+@pytest.mark.parametrize("M,N", [(3, 70), (130, 333), (700, 2050), (2100, 2300)])
+def test_strides(fmt, M, N):
+    """y, residual and gate as parts of wider tensors, at odd places; neighbours untouched."""
+    K, groups = 256, 2 if M % 2 == 0 else 1
+    f, _, args, v, mag = operands(fmt, M, N, K, M)
+    g = torch.Generator().manual_seed(M)
+    wide_y = torch.full((M, N + 11), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide_r, wide_g = bf(g, M, N + 5), bf(g, groups, 3 * N)
+    gate, residual, bias = wide_g[:, N:2 * N], wide_r[:, :N], bf(g, N + 1)[1:]
+    group = np.arange(M) // (M // groups)
+    y = f(*args, bias=bias, act=ACTS["silu"], gate=gate, residual=residual, y=wide_y[:, :N])
+    check(y, v, mag, K, bias, "silu", gate, residual, group)
+    assert torch.all(wide_y[:, N:] == 7.0)
+    wide_y = torch.full((M, N + 11), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide_y[:, :N] = residual
+    f(*args, bias=bias, act=ACTS["silu"], gate=gate, residual=wide_y[:, :N], y=wide_y[:, :N])
+    assert torch.equal(wide_y[:, :N], y) and torch.all(wide_y[:, N:] == 7.0)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu"])
+def test_activations_over_their_range(act):
+    """v from far below to far above, by a bias on a product of zeros."""
+    M, N, K = 2, 4096, 256
+    v = torch.cat([torch.linspace(-30, 30, N - 11), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 200.0, -200.0, 3e38, -3e38,
+                                                                  float("inf"), -4.99, -5.01])]).bfloat16()
+    zero = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    w = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    y = f64(L.bsq_gemm_fp8r_q_epilogue(zero, torch.ones(M, device="cuda"), w, torch.ones(N, device="cuda"), bias=v.cuda(),
+                                       act=ACTS[act]))
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref = block.activation(f64(v), act)
+    ref = np.where(np.isposinf(f64(v)), np.inf, ref)
+    far = f64(v) < -1e30
+    ok = np.abs(y - ref) <= (2.0 ** -8 + 2.0 ** -15) * np.abs(ref) + (4e-7 if act == "gelu" else 2.0 ** -120)
+    assert np.all(ok | (y == ref) | (far & (y == 0)))
+
+
+def test_odd_values_stay_where_they_are():
+    """NaN and infinities in residual, gate and bias reach their own outputs only."""
+    for M, N in ((5, 200), (300, 520)):
+        f, _, args, v, mag = operands("fp8r", M, N, 256, 1)
+        g = torch.Generator().manual_seed(2)
+        bias, gate, residual = bf(g, N), bf(g, 1, N), bf(g, M, N)
+        want = f(*args, bias=bias, gate=gate, residual=residual)
+        bias[3], gate[0, 9], residual[2, 17] = float("nan"), float("inf"), float("-inf")
+        got = f(*args, bias=bias, gate=gate, residual=residual)
+        hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+        hit[:, 3] = hit[:, 9] = hit[2, 17] = True
+        assert torch.equal(got[~hit], want[~hit])
+        assert torch.isnan(got[:, 3]).all() and not torch.isfinite(got[:, 9]).any() and got[2, 17] == float("-inf")
+
+
+def test_starts_out_of_range_stay_inside():
+    """What rows get for starts that decrease or leave the rows is not defined; memory around y is left alone."""
+    for M, N in ((20, 192), (300, 520)):
+        f, _, args, _, _ = operands("fp8r", M, N, 256, 1)
+        gate = torch.randn(4, N, device="cuda").bfloat16()
+        for starts in ([5, 3, 9, 2, 4000], [-9, -3, 50, 7, M], [0, 1000, 2000, 3000, 1 << 30], [M, 0, M, 0, M], [0, 8, 16, 17, -1]):
+            pad = torch.full((3, M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+            f(*args, gate=gate, starts=torch.tensor(starts, dtype=torch.int32).cuda(), y=pad[1])
+            torch.cuda.synchronize()
+            assert torch.all(pad[0] == 7.0) and torch.all(pad[2] == 7.0)
+
+
+@pytest.mark.parametrize("fmt", ["fp8r", "nvfp4"])
+def test_captured_and_replayed(fmt):
+    for M, N in ((8, 512), (500, 1000)):
+        f, _, args, _, _ = operands(fmt, M, N, 512, 3)
+        g = torch.Generator().manual_seed(4)
+        bias, gate, residual = bf(g, N), bf(g, 3, N), bf(g, M, N)
+        st = torch.tensor([0, 1, 5, M], dtype=torch.int32).cuda()
+        more = dict(bias=bias, act=ACTS["gelu"], gate=gate, residual=residual, starts=st)
+        f(*args, **more)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = f(*args, **more)
+        for i in range(4):
+            residual.normal_()
+            gate.normal_()
+            st.copy_(torch.tensor([0, i, 5 + i // 2, M]))
+            graph.replay()
+            want = f(*args, **more)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want), i
