@@ -65,15 +65,8 @@ struct Epilogue {
   const uint16_t* residual;  // [M] rows residual_stride apart, or null
   int64_t residual_stride;
   RowGroups groups;
-  int act;       // bsq_act
-  float c0, c1;  // of the activations that have two coefficients (epilogue.hpp)
+  int act;  // bsq_act
 };
-// the coefficients of an activation that has two
-inline void act_coefficients(Epilogue& e) {
-  const double log2e = 1.4426950408889634, k = -2.0 * log2e * 0.7978845608028654;
-  e.c0 = (float)(e.act == BSQ_ACT_SILU ? -log2e : k);
-  e.c1 = (float)(e.act == BSQ_ACT_SILU ? 0.0 : k * 0.044715);
-}
 // the few-token kernels (W8A8, W4A4), the tiled W8A8 ones, the tiled W4A4 ones (K % 256 == 0, and any K)
 hipError_t launch_gemm_skinny_epilogue(DecMode mode, const DecArgs& a, const Epilogue& ep, hipStream_t s);
 hipError_t launch_gemm_fp8_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s);

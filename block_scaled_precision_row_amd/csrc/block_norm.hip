@@ -1,9 +1,10 @@
 // The gated residual with the norms before and after it, and its gradient (include/bsq_block.h).
 //
-// Bound by memory: a row is read once, held in fp32 registers by the W waves of one worker (chunk lane + 64 (wave + W k)
-// of eight elements, k < C), and written once. The vectors of its group are read again for every row, from the caches.
-// A sum over the row is one DPP reduction in each wave and, with W > 1, one exchange through LDS; the variance is taken
-// about the mean (a second reduction) rather than from the squares, which would cancel for rows far from zero.
+// Bound by memory: a row is read once, held in fp32 registers by the waves of one worker, and written once; a worker
+// takes several rows, with the next one's loads under way while it computes one, and keeps the vectors of its group in
+// registers. A sum over the row is one DPP reduction in each wave and, where a worker has several, one exchange through
+// LDS; the variance is taken about the mean (a second reduction) rather than from the squares, which would cancel for
+// rows far from zero.
 #include <type_traits>
 #include <utility>
 
@@ -17,76 +18,164 @@ namespace {
 // ---- sums over a row --------------------------------------------------------------
 
 template <int ctrl, int rows>
-__device__ __forceinline__ float dpp_from(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, rows, 0xF, false));
+__device__ __forceinline__ uint32_t dpp_from(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false);
 }
-// over the wave's 64 lanes, the same in all of them
+template <int ctrl, int rows>
+__device__ __forceinline__ uint32_t max_from(uint32_t v) {
+  const uint32_t o = dpp_from<ctrl, rows>(v);
+  return o > v ? o : v;
+}
+template <int ctrl, int rows>
+__device__ __forceinline__ float add_from(float v) {
+  return v + __uint_as_float(dpp_from<ctrl, rows>(__float_as_uint(v)));
+}
+__device__ __forceinline__ float row_sum(float v) {  // over 16 lanes, in the last of them: row_shr 1, 2, 4, 8
+  return add_from<0x118, 0xF>(add_from<0x114, 0xF>(add_from<0x112, 0xF>(add_from<0x111, 0xF>(v))));
+}
+// Over the wave's 64 lanes, the same in all of them (row_bcast 15: rows 0 and 2 to 1 and 3; row_bcast 31: the first half
+// to the second). On the matrix cores (v as a 16 x 4 operand against ones, twice) this is 5 instructions rather than 14,
+// but takes longer: the gradient at 4608 x 2560 53 us against 47.
 __device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_from<0x111, 0xF>(v);  // within 16 lanes: row_shr 1, 2, 4, 8
-  v += dpp_from<0x112, 0xF>(v);
-  v += dpp_from<0x114, 0xF>(v);
-  v += dpp_from<0x118, 0xF>(v);
-  v += dpp_from<0x142, 0xA>(v);  // row_bcast 15: rows 0 and 2 to 1 and 3
-  v += dpp_from<0x143, 0xC>(v);  // row_bcast 31: the first half to the second
+  v = add_from<0x143, 0xC>(add_from<0x142, 0xA>(row_sum(v)));
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
-// the larger, NaN if either is NaN
-__device__ __forceinline__ float max_nan(float a, float b) { return a != a || a > b ? a : b; }
-__device__ __forceinline__ float wave_max_nan(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = max_nan(v, __shfl_xor(v, off, 64));
-  return v;
+// the largest, likewise
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max_from<0x118, 0xF>(max_from<0x114, 0xF>(max_from<0x112, 0xF>(max_from<0x111, 0xF>(v))));
+  v = max_from<0x143, 0xC>(max_from<0x142, 0xA>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Sums (or the maximum) over the W waves of a worker. Each reduction of a row has LDS of its own, and rows alternate between two sets of
-// it: a wave that is a row ahead has passed a barrier that the others reach only after they have read the set before.
+// Sums (or the maximum) over the waves of a worker: over the lanes, then through LDS, where each reduction of a row has
+// room of its own and rows alternate between two sets of it: a wave that is a row ahead has passed a barrier that the
+// others reach only after they have read the set before. ONE: the worker is one wave.
 constexpr int kReductions = 6, kMostSums = 2;  // of a row at most: two norms of two each, and one for each gradient
-template <int W>
+constexpr int kMostWaves = 16;
+struct Slots {
+  float s[2][kReductions][kMostSums][kMostWaves];
+};
+template <bool ONE>
 struct RowSums {
-  float (*slots)[W][kMostSums];  // [kReductions] of this row's parity
-  int wave, lane, at;
+  Slots* slots;
+  int wave, waves, lane, row, at;
   template <int K>
   __device__ __forceinline__ void sum(float (&v)[K]) {
     static_assert(K <= kMostSums, "room");
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
-    if constexpr (W > 1) {
-      float(*s)[kMostSums] = slots[at++];
+    if constexpr (!ONE) {
+      auto& s = slots->s[row & 1][at++];
       if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) s[wave][k] = v[k];
+        for (int k = 0; k < K; ++k) s[k][wave] = v[k];
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        v[k] = s[0][k];
-#pragma unroll
-        for (int w = 1; w < W; ++w) v[k] += s[w][k];
+      for (int k = 0; k < K; ++k) {  // (the first 16 lanes)
+        const float o = row_sum(lane < waves ? s[k][lane & (kMostWaves - 1)] : 0.0f);
+        v[k] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(o), kMostWaves - 1));
       }
     }
   }
-  __device__ __forceinline__ float max(float v) {
-    v = wave_max_nan(v);
-    if constexpr (W > 1) {
-      float(*s)[kMostSums] = slots[at++];
-      if (lane == 0) s[wave][0] = v;
+  __device__ __forceinline__ float max(float most) {  // of magnitudes: their bits order as they do, NaN above all
+    uint32_t v = wave_max(__float_as_uint(most));
+    if constexpr (!ONE) {
+      auto& s = slots->s[row & 1][at++];
+      if (lane == 0) s[0][wave] = __uint_as_float(v);
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < W; ++w) v = max_nan(v, s[w][0]);
+      v = wave_max(lane < waves ? __float_as_uint(s[0][lane & (kMostWaves - 1)]) : 0u);
     }
-    return v;
+    return __uint_as_float(v);
   }
 };
 
-template <int W>
-constexpr int threads_of() { return W == 1 ? 256 : 64 * W; }
-template <int W>
-constexpr int workers_of() { return W == 1 ? 4 : 1; }  // in a workgroup
+// ---- a worker's piece of a row --------------------------------------------------------
+
+// A worker's waves share a row: chunk lane + 64 (wave + waves k) of eight elements, k < C. One wave takes rows of up to
+// 512 elements, four such workers in a workgroup; longer rows have a workgroup of up to eight waves.
+template <bool ONE>
+constexpr int most_threads() { return ONE ? 256 : 64 * kMostWaves; }
+constexpr int kBackwardThreads = 512;
+
+template <class E>
+struct Chunk {  // eight elements as they are in memory
+  uint4 q;
+  __device__ __forceinline__ void load(const typename E::elem* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8<E>(q, f); }
+};
+template <>
+struct Chunk<Fp32> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+
+template <bool ONE, int C>
+struct Place {
+  int worker, part, parts, lane;
+  uint32_t at[C];  // first element of the chunk
+  bool has[C];
+  __device__ __forceinline__ Place(int dim) {
+    lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    worker = ONE ? blockIdx.x * 4 + wave : blockIdx.x;
+    part = ONE ? 0 : wave;
+    parts = ONE ? 1 : __builtin_amdgcn_readfirstlane((int)blockDim.x >> 6);
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const int c = lane + 64 * (part + parts * k);
+      has[k] = c < dim >> 3;
+      at[k] = 8u * (uint32_t)c;
+    }
+  }
+  // the worker's chunks of the row behind p (zeros where it has none, or without a row)
+  template <class E>
+  __device__ __forceinline__ void load(Chunk<E> (&r)[C], const typename E::elem* p) const {
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      r[k].zero();
+      if (p && has[k]) r[k].load(p + at[k]);
+    }
+  }
+};
+
+// A vector along the row: held in registers from row to row, or read again for each (HOLD: registers allow it)
+template <class E, int C, bool HOLD>
+struct Vector {
+  const typename E::elem* p;
+  Chunk<E> r[HOLD ? C : 1];
+  template <class P>
+  __device__ __forceinline__ void set(const P& me, const typename E::elem* to) {
+    p = to;
+    if constexpr (HOLD) me.load(r, to);
+  }
+  // chunk k as fp32, of a vector that is there (anything where the worker has no chunk)
+  template <class P>
+  __device__ __forceinline__ void get(const P& me, int k, float (&f)[8]) const {
+    if constexpr (HOLD) {
+      r[k].get(f);
+    } else {
+      Chunk<E> c;
+      c.zero();
+      if (me.has[k]) c.load(p + me.at[k]);
+      c.get(f);
+    }
+  }
+};
 
 // v becomes v - mean (BSQ_NORM_LAYER); returns 1 / sqrt(mean v^2 + eps)
-template <int W, int C>
+template <bool ONE, int C>
 __device__ __forceinline__ float size_of(float (&v)[C][8], bool layer, float eps, float inv_dim, const bool (&has)[C],
-                                         RowSums<W>& rs) {
+                                         RowSums<ONE>& rs) {
   if (layer) {
     float s[1] = {0.0f};
 #pragma unroll
@@ -111,11 +200,19 @@ __device__ __forceinline__ float size_of(float (&v)[C][8], bool layer, float eps
 
 template <class E>
 __device__ __forceinline__ const typename E::elem* row_of(const Rows& r, int64_t row) {
-  return static_cast<const typename E::elem*>(r.p) + row * r.stride;
+  return r.p ? static_cast<const typename E::elem*>(r.p) + row * r.stride : nullptr;
+}
+template <class E>
+__device__ __forceinline__ typename E::elem* out_of(const Rows& r, int64_t row) {
+  return static_cast<typename E::elem*>(r.p) + row * r.stride;
 }
 template <class E>
 __device__ __forceinline__ const typename E::elem* row_of(const GroupVector& v, int g) {
-  return static_cast<const typename E::elem*>(v.p) + (int64_t)g * v.stride;
+  return v.p ? static_cast<const typename E::elem*>(v.p) + (int64_t)g * v.stride : nullptr;
+}
+template <class E>
+__device__ __forceinline__ const typename E::elem* row_of(const void* v) {
+  return static_cast<const typename E::elem*>(v);
 }
 
 // ---- forward ------------------------------------------------------------------------
@@ -129,105 +226,121 @@ __device__ __forceinline__ uint32_t block_scale(float a, float G, float& r) {
   return sf;
 }
 
-template <class E, int W, int C>
-__global__ __launch_bounds__(threads_of<W>()) void block_norm(NormForward a) {
+// the larger of two magnitudes, NaN if one is (one instruction, of three operands)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// One row a worker: with some 20 waves on a compute unit the loads of other rows run under a row's sums.
+template <class E, bool ONE, int C, bool GROUPED>
+__global__ __launch_bounds__(most_threads<ONE>()) void block_norm(NormForward a) {
   typedef typename E::elem elem;
-  __shared__ float slots[W > 1 ? kReductions : 1][W][kMostSums];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int row = blockIdx.x * workers_of<W>() + (W == 1 ? wave : 0);
-  const int part = W == 1 ? 0 : wave;
+  __shared__ Slots slots;
   const NormArgs& n = a.n;
-  if (row >= group_limit(n.groups)) return;  // (the whole worker)
-  const int chunks = n.dim >> 3;
-  const float inv_dim = 1.0f / (float)n.dim;
-  RowSums<W> rs{slots, part, lane, 0};
-  int at[C];
-  bool has[C];
-  float v[C][8];
-  const elem* x = row_of<E>(a.x, row);
-#pragma unroll
-  for (int k = 0; k < C; ++k) {
-    const int c = lane + 64 * (part + W * k);
-    has[k] = c < chunks;
-    at[k] = 8 * c;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
-    if (has[k]) load8<E>(x + at[k], v[k]);
+  const Place<ONE, C> me(n.dim);
+  const int row = me.worker;
+  if (row >= n.groups.rows) return;  // (the whole worker)
+  Chunk<E> x[C], h[C];
+  me.load(x, row_of<E>(a.x, row));
+  me.load(h, row_of<E>(a.branch, row));
+  Vector<E, C, !GROUPED> weight, bias, pw;
+  pw.set(me, row_of<E>(n.post_weight));
+  weight.set(me, row_of<E>(n.weight));
+  bias.set(me, row_of<E>(n.bias));
+  if (row >= group_limit(n.groups)) return;
+  const int g = GROUPED ? group_of_wave(n.groups, row, me.lane) : 0;
+  Vector<E, C, false> scale, shift, gate;
+  if constexpr (GROUPED) {
+    gate.set(me, row_of<E>(n.gate, g));
+    scale.set(me, row_of<E>(n.scale, g));
+    shift.set(me, row_of<E>(n.shift, g));
   }
-  const int g = n.scale.p || n.shift.p || n.gate.p ? group_of_wave(n.groups, row, lane) : 0;
+  const float inv_dim = 1.0f / (float)n.dim;
+  RowSums<ONE> rs{&slots, me.part, me.parts, me.lane, 0, 0};
+  float v[C][8];
+#pragma unroll
+  for (int k = 0; k < C; ++k) x[k].get(v[k]);
   if (a.branch.p) {
-    float h[C][8];
-    const elem* b = row_of<E>(a.branch, row);
+    float f[C][8];
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = 0.0f;
-      if (has[k]) load8<E>(b + at[k], h[k]);
-    }
+    for (int k = 0; k < C; ++k) h[k].get(f[k]);
     if (n.post != BSQ_NORM_NONE) {
-      const float r = size_of<W, C>(h, n.post == BSQ_NORM_LAYER, n.post_eps, inv_dim, has, rs);
+      const float r = size_of<ONE, C>(f, n.post == BSQ_NORM_LAYER, n.post_eps, inv_dim, me.has, rs);
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-        if (n.post_weight && has[k]) load8<E>(static_cast<const elem*>(n.post_weight) + at[k], w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[k][e] = h[k][e] * r * w[e];
+        for (int e = 0; e < 8; ++e) f[k][e] *= r;
+        if (pw.p) {
+          float w[8];
+          pw.get(me, k, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[k][e] *= w[e];
+        }
       }
     }
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      if (!has[k]) continue;
-      float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-      if (n.gate.p) load8<E>(row_of<E>(n.gate, g) + at[k], w);
+      if (GROUPED && gate.p) {
+        float w[8];
+        gate.get(me, k, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = fmaf(w[e], h[k][e], v[k][e]);
-      if (a.x_out.p) store8<E>(const_cast<elem*>(row_of<E>(a.x_out, row)) + at[k], v[k]);
+        for (int e = 0; e < 8; ++e) v[k][e] = fmaf(w[e], f[k][e], v[k][e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] += f[k][e];
+      }
+      if (a.x_out.p && me.has[k]) store8<E>(out_of<E>(a.x_out, row) + me.at[k], v[k]);
     }
   }
   if (n.norm == BSQ_NORM_NONE) return;
-  const float r = size_of<W, C>(v, n.norm == BSQ_NORM_LAYER, n.eps, inv_dim, has, rs);
+  const float r = size_of<ONE, C>(v, n.norm == BSQ_NORM_LAYER, n.eps, inv_dim, me.has, rs);
   float most = 0.0f;
 #pragma unroll
   for (int k = 0; k < C; ++k) {
-    if (!has[k]) continue;
-    float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-    if (n.weight) load8<E>(static_cast<const elem*>(n.weight) + at[k], w);
+    if (!me.has[k]) continue;
+    float w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * r * w[e];
-    if (n.bias) {
-      load8<E>(static_cast<const elem*>(n.bias) + at[k], w);
+    for (int e = 0; e < 8; ++e) v[k][e] *= r;
+    if (weight.p) {
+      weight.get(me, k, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] *= w[e];
+    }
+    if (bias.p) {
+      bias.get(me, k, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[k][e] += w[e];
     }
-    if (n.scale.p) {
-      load8<E>(row_of<E>(n.scale, g) + at[k], w);
+    if constexpr (GROUPED) {
+      if (scale.p) {
+        scale.get(me, k, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] *= 1.0f + w[e];
+        for (int e = 0; e < 8; ++e) v[k][e] = fmaf(v[k][e], w[e], v[k][e]);  // (v (1 + scale))
+      }
+      if (shift.p) {
+        shift.get(me, k, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] += w[e];
+      }
     }
-    if (n.shift.p) {
-      load8<E>(row_of<E>(n.shift, g) + at[k], w);
+    if (a.out_format == 0) {
+      store8<E>(out_of<E>(a.y, row) + me.at[k], v[k]);
+    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] += w[e];
+      for (int e = 0; e < 8; e += 2) most = larger(larger(most, fabsf(v[k][e])), fabsf(v[k][e + 1]));
     }
-    if (a.out_format == 0) store8<E>(const_cast<elem*>(row_of<E>(a.y, row)) + at[k], v[k]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) most = max_nan(most, fabsf(v[k][e]));
   }
   if (a.out_format == BSQ_FMT_FP8R) {
-    most = rs.max(most);
-    const float d = most / kE4M3Max;
+    const float d = rs.max(most) / kE4M3Max;
     const float q = d > 0.0f ? 1.0f / d : (d != d ? d : 0.0f);
     uint8_t* y = static_cast<uint8_t*>(a.y.p) + (int64_t)row * n.dim;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      if (!has[k]) continue;
+      if (!me.has[k]) continue;
       uint2 o;
       o.x = enc_e4m3x4(v[k][0] * q, v[k][1] * q, v[k][2] * q, v[k][3] * q);
       o.y = enc_e4m3x4(v[k][4] * q, v[k][5] * q, v[k][6] * q, v[k][7] * q);
-      *reinterpret_cast<uint2*>(y + at[k]) = o;
+      *reinterpret_cast<uint2*>(y + me.at[k]) = o;
     }
-    if (part == 0 && lane == 0) static_cast<float*>(a.y_scale)[row] = d;
+    if (me.part == 0 && me.lane == 0) static_cast<float*>(a.y_scale)[row] = d;
   }
   if (a.out_format == BSQ_FMT_NVFP4) {
     const float G = 1.0f / a.y_global[0];
@@ -237,16 +350,16 @@ __global__ __launch_bounds__(threads_of<W>()) void block_norm(NormForward a) {
     for (int k = 0; k < C; ++k) {
       float m = 0.0f;  // of the lane's half of a block of 16; its neighbour has the other (dim % 16 == 0: both or none)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(v[k][e]));
-      m = max_nan(m, __shfl_xor(m, 1, 64));
-      if (!has[k]) continue;
+      for (int e = 0; e < 8; e += 2) m = larger(larger(m, fabsf(v[k][e])), fabsf(v[k][e + 1]));
+      m = larger(m, __uint_as_float(dpp_from<0xB1, 0xF>(__float_as_uint(m))));  // quad_perm 1, 0, 3, 2
+      if (!me.has[k]) continue;
       float q;
       const uint32_t sf = block_scale(m, G, q);
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = v[k][e] * q;
-      *reinterpret_cast<uint32_t*>(y + (at[k] >> 1)) = enc_e2m1x8(f);
-      if ((lane & 1) == 0) ys[at[k] >> 4] = (uint8_t)sf;
+      *reinterpret_cast<uint32_t*>(y + (me.at[k] >> 1)) = enc_e2m1x8(f);
+      if ((me.lane & 1) == 0) ys[me.at[k] >> 4] = (uint8_t)sf;
     }
   }
 }
@@ -257,136 +370,149 @@ __global__ __launch_bounds__(threads_of<W>()) void block_norm(NormForward a) {
 // workspace, [slot][3][dim] (no two have the same: the group grows from slot to slot where the worker does not). A
 // second kernel adds the slots of each group in their order, and a third the groups for the gradients that all share.
 
-template <class E, int W, int C>
-__global__ __launch_bounds__(threads_of<W>()) void block_norm_backward(NormBackward a, int run, float* part_sums) {
+enum { kSumScale = 1, kSumShift = 2, kSumGate = 4 };  // which of the three sums a call needs
+
+template <class E, bool ONE, int C, bool GROUPED>
+__global__ __launch_bounds__(ONE ? 256 : kBackwardThreads) void block_norm_backward(NormBackward a, int run, int need,
+                                                                           float* part_sums) {
   typedef typename E::elem elem;
-  __shared__ float slots[W > 1 ? 2 * kReductions : 1][W][kMostSums];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int worker = blockIdx.x * workers_of<W>() + (W == 1 ? wave : 0);
-  const int part = W == 1 ? 0 : wave;
+  __shared__ Slots slots;
   const NormArgs& n = a.n;
-  const int limit = group_limit(n.groups), first = worker * run;
+  const Place<ONE, C> me(n.dim);
+  const int first = me.worker * run, limit = group_limit(n.groups);
   const int last = limit - first < run ? limit : first + run;
-  if (first >= last) return;
-  const int chunks = n.dim >> 3;
+  if (first >= last) return;  // (the whole worker)
   const float inv_dim = 1.0f / (float)n.dim;
   const bool layer = n.norm == BSQ_NORM_LAYER, post_layer = n.post == BSQ_NORM_LAYER;
   const bool normed = n.norm != BSQ_NORM_NONE, post = n.post != BSQ_NORM_NONE, branch = a.branch.p != nullptr;
-  int at[C];
-  bool has[C];
   float sums[3][C][8];
 #pragma unroll
-  for (int k = 0; k < C; ++k) {
-    const int c = lane + 64 * (part + W * k);
-    has[k] = c < chunks;
-    at[k] = 8 * c;
+  for (int k = 0; k < C; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[0][k][e] = sums[1][k][e] = sums[2][k][e] = 0.0f;
-  }
   auto flush = [&](int g) {
-    float* to = part_sums + (int64_t)(worker + g) * 3 * n.dim;
+    float* to = part_sums + (int64_t)(me.worker + g) * 3 * n.dim;
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        if (has[k]) store8<Fp32>(to + (int64_t)q * n.dim + at[k], sums[q][k]);
+        if ((need >> q & 1) && me.has[k]) store8<Fp32>(to + (int64_t)q * n.dim + me.at[k], sums[q][k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[q][k][e] = 0.0f;
       }
   };
-  auto load = [&](const elem* p, float (&f)[C][8]) {
+  constexpr bool kAhead = C <= 2;  // the next row's loads, while registers allow it
+  Chunk<E> x[C], dy[C], dx[C], h[C];
+  Vector<E, C, C <= 2 && !GROUPED> weight, pw;
+  Vector<E, C, C <= 2 && GROUPED> scale, gate;
+  auto load_row = [&](int row) {
+    me.load(x, normed ? row_of<E>(a.x_out, row) : nullptr);
+    me.load(dy, normed ? row_of<E>(a.dy, row) : nullptr);
+    me.load(h, row_of<E>(a.branch, row));
+    me.load(dx, row_of<E>(a.dx_out, row));
+  };
+  load_row(first);
+  weight.set(me, row_of<E>(n.weight));
+  pw.set(me, row_of<E>(n.post_weight));
+  int g = GROUPED ? -1 : 0, end = first;  // (without vectors of groups all rows count as one's)
+  for (int row = first; row < last; ++row) {
+    if (GROUPED && row >= end) {
+      if (g >= 0 && need) flush(g);
+      g = group_of_wave(n.groups, row, me.lane);
+      end = group_end(n.groups, g);
+      scale.set(me, row_of<E>(n.scale, g));
+      gate.set(me, row_of<E>(n.gate, g));
+    }
+    if (!kAhead && row > first) load_row(row);
+    RowSums<ONE> rs{&slots, me.part, me.parts, me.lane, row, 0};
+    float c[C][8], v[C][8], d[C][8], f[C][8];
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[k][e] = 0.0f;
-      if (has[k]) load8<E>(p + at[k], f[k]);
+      dx[k].get(c[k]);
+      x[k].get(v[k]);
+      dy[k].get(d[k]);
+      h[k].get(f[k]);
     }
-  };
-  int g = group_of_wave(n.groups, first, lane);
-  for (int row = first; row < last; ++row) {
-    if (row > first && n.groups.groups > 1) {
-      const int now = group_of_wave(n.groups, row, lane);
-      if (now != g) {
-        if (part_sums) flush(g);
-        g = now;
-      }
-    }
-    RowSums<W> rs{slots + (W > 1 ? (row & 1) * kReductions : 0), part, lane, 0};
-    float c[C][8], v[C][8], d[C][8], h[C][8];
-    if (a.dx_out.p) load(row_of<E>(a.dx_out, row), c);
-    else
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] = 0.0f;
-    if (branch) load(row_of<E>(a.branch, row), h);
-    float hr = 1.0f;
+    if (kAhead && row + 1 < last) load_row(row + 1);
+    float hr = 1.0f, r = 0.0f, along = 0.0f, mean = 0.0f;
     if (branch && post) {
-      hr = size_of<W, C>(h, post_layer, n.post_eps, inv_dim, has, rs);
+      hr = size_of<ONE, C>(f, post_layer, n.post_eps, inv_dim, me.has, rs);
 #pragma unroll
       for (int k = 0; k < C; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[k][e] *= hr;
+        for (int e = 0; e < 8; ++e) f[k][e] *= hr;
     }
     if (normed) {
-      load(row_of<E>(a.x_out, row), v);
-      load(row_of<E>(a.dy, row), d);
-      const float r = size_of<W, C>(v, layer, n.eps, inv_dim, has, rs);
+      r = size_of<ONE, C>(v, layer, n.eps, inv_dim, me.has, rs);
       float s[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        float w[8] = {1, 1, 1, 1, 1, 1, 1, 1}, m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (n.weight && has[k]) load8<E>(static_cast<const elem*>(n.weight) + at[k], w);
-        if (n.scale.p && has[k]) load8<E>(row_of<E>(n.scale, g) + at[k], m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] *= r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          v[k][e] *= r;
           sums[0][k][e] = fmaf(d[k][e], v[k][e], sums[0][k][e]);
           sums[1][k][e] += d[k][e];
-          d[k][e] *= (1.0f + m[e]) * w[e];
+        }
+        float w[8];
+        if (GROUPED && scale.p) {
+          scale.get(me, k, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[k][e] = fmaf(d[k][e], w[e], d[k][e]);
+        }
+        if (weight.p) {
+          weight.get(me, k, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[k][e] *= w[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
           s[0] = fmaf(d[k][e], v[k][e], s[0]);
           s[1] += d[k][e];
         }
       }
       rs.sum(s);
-      const float along = s[0] * inv_dim, mean = layer ? s[1] * inv_dim : 0.0f;
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] = fmaf(r, d[k][e] - mean - v[k][e] * along, c[k][e]);
+      along = s[0] * inv_dim;
+      mean = layer ? s[1] * inv_dim : 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      if (!has[k]) {
+      if (normed) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[k][e] = fmaf(r, d[k][e] - mean - v[k][e] * along, c[k][e]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      if (!me.has[k]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) c[k][e] = 0.0f;
       }
-      if (a.dx.p && has[k]) store8<E>(const_cast<elem*>(row_of<E>(a.dx, row)) + at[k], c[k]);
+      if (a.dx.p && me.has[k]) store8<E>(out_of<E>(a.dx, row) + me.at[k], c[k]);
       if (branch) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[2][k][e] = fmaf(c[k][e], h[k][e], sums[2][k][e]);
+        for (int e = 0; e < 8; ++e) sums[2][k][e] = fmaf(c[k][e], f[k][e], sums[2][k][e]);
       }
     }
     if (!a.dbranch.p) continue;
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-      if (n.gate.p && has[k]) {
-        load8<E>(row_of<E>(n.gate, g) + at[k], w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] *= w[e];
-      }
-      if (post && n.post_weight && has[k]) {
-        load8<E>(static_cast<const elem*>(n.post_weight) + at[k], w);
+      float w[8];
+      if (GROUPED && gate.p) {
+        gate.get(me, k, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) c[k][e] *= w[e];
       }
       if (post) {
+        if (pw.p) {
+          pw.get(me, k, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c[k][e] *= w[e];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s[0] = fmaf(c[k][e], h[k][e], s[0]);
+          s[0] = fmaf(c[k][e], f[k][e], s[0]);
           s[1] += c[k][e];
         }
       }
@@ -397,13 +523,13 @@ __global__ __launch_bounds__(threads_of<W>()) void block_norm_backward(NormBackw
 #pragma unroll
       for (int k = 0; k < C; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] = hr * (c[k][e] - mean - h[k][e] * along);
+        for (int e = 0; e < 8; ++e) c[k][e] = hr * (c[k][e] - mean - f[k][e] * along);
     }
 #pragma unroll
     for (int k = 0; k < C; ++k)
-      if (has[k]) store8<E>(const_cast<elem*>(row_of<E>(a.dbranch, row)) + at[k], c[k]);
+      if (me.has[k]) store8<E>(out_of<E>(a.dbranch, row) + me.at[k], c[k]);
   }
-  if (part_sums) flush(g);
+  if (need) flush(g);
 }
 
 template <class E>
@@ -411,88 +537,114 @@ __device__ __forceinline__ float one(const void* p, int64_t at) {
   if constexpr (sizeof(typename E::elem) == 4) return static_cast<const float*>(p)[at];
   else return E::up(static_cast<const uint16_t*>(p)[at]);
 }
-template <class E>
-__device__ __forceinline__ float one(const GroupVector& v, int g, int col) {
-  return one<E>(v.p, (int64_t)g * v.stride + col);
-}
+// Columns are taken four at a time, by 8 x 8 lanes of a wave (quadruple, share) and 16 waves: 128 threads share the sum of
+// a column, so that a few hundred slots are a few loads each.
+constexpr int kCols = 8, kWaves = 16, kShares = 8 * kWaves;
 
-constexpr int kCols = 32, kLanes = 32;  // columns of a workgroup, and threads that share a column's sum
-
-// the sum over the threads of a column, in all of them (sum[][] is free again after it)
-__device__ __forceinline__ float column_sum(float v, float (*sum)[kCols], int col, int lane) {
-  sum[lane][col] = v;
-  __syncthreads();
+__device__ __forceinline__ void add4(float4& a, float4 b) { a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+// sums[q] over the threads of a column: whole in the first 8 threads of the workgroup
+struct ColumnSlots {
+  float4 s[3][kWaves][kCols];
+};
+__device__ __forceinline__ void column_sums(float4 (&v)[3], int need, ColumnSlots& slots) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int s = kLanes / 2; s >= 1; s >>= 1) {
-    if (lane < s) sum[lane][col] += sum[lane + s][col];
-    __syncthreads();
+  for (int q = 0; q < 3; ++q) {
+    if (!(need >> q & 1)) continue;
+#pragma unroll
+    for (int off = 8; off <= 32; off <<= 1)
+      add4(v[q], make_float4(__shfl_xor(v[q].x, off, 64), __shfl_xor(v[q].y, off, 64), __shfl_xor(v[q].z, off, 64),
+                             __shfl_xor(v[q].w, off, 64)));
+    if (lane < kCols) slots.s[q][wave][lane] = v[q];
   }
-  v = sum[0][col];
   __syncthreads();
-  return v;
+  if (threadIdx.x < kCols) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      if (!(need >> q & 1)) continue;
+      v[q] = slots.s[q][0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) add4(v[q], slots.s[q][w][threadIdx.x]);
+    }
+  }
+  __syncthreads();  // (the slots are free again)
+}
+__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
+  return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z), fmaf(a.w, b.w, c.w));
+}
+template <class E>
+__device__ __forceinline__ float4 four(const void* p, int64_t at) {
+  return make_float4(one<E>(p, at), one<E>(p, at + 1), one<E>(p, at + 2), one<E>(p, at + 3));
+}
+__device__ __forceinline__ void put4(float* p, int64_t at, float4 v) {  // (gradients are 4-byte aligned)
+  p[at] = v.x; p[at + 1] = v.y; p[at + 2] = v.z; p[at + 3] = v.w;
 }
 
 // the gradients that all groups share, from the sums of one group (or of all)
 template <class E>
-__device__ __forceinline__ void add_shared(const NormBackward& a, int g, int col, const float (&s)[3], float (&t)[3]) {
-  const float m = a.n.scale.p ? 1.0f + one<E>(a.n.scale, g, col) : 1.0f;
-  const float k = a.n.gate.p ? one<E>(a.n.gate, g, col) : 1.0f;
-  t[0] = fmaf(m, s[0], t[0]);
-  t[1] = fmaf(m, s[1], t[1]);
-  t[2] = fmaf(k, s[2], t[2]);
+__device__ __forceinline__ void add_shared(const NormBackward& a, int g, int col, const float4 (&s)[3], float4 (&t)[3]) {
+  float4 m = make_float4(1, 1, 1, 1), k = m;
+  if (a.n.scale.p) add4(m, four<E>(a.n.scale.p, (int64_t)g * a.n.scale.stride + col));
+  if (a.n.gate.p) k = four<E>(a.n.gate.p, (int64_t)g * a.n.gate.stride + col);
+  t[0] = fma4(m, s[0], t[0]);
+  t[1] = fma4(m, s[1], t[1]);
+  t[2] = fma4(k, s[2], t[2]);
 }
-__device__ __forceinline__ void put_shared(const NormBackward& a, int col, const float (&t)[3]) {
-  if (a.dweight) a.dweight[col] = t[0];
-  if (a.dbias) a.dbias[col] = t[1];
-  if (a.dpost_weight) a.dpost_weight[col] = t[2];
+__device__ __forceinline__ void put_shared(const NormBackward& a, int col, const float4 (&t)[3]) {
+  if (a.dweight) put4(a.dweight, col, t[0]);
+  if (a.dbias) put4(a.dbias, col, t[1]);
+  if (a.dpost_weight) put4(a.dpost_weight, col, t[2]);
 }
 
 // The sums of each group: grid.x over columns, grid.y (striding) over groups. With one group also what all groups share;
 // otherwise, where that is asked for, the sums go to `group_sums` [groups][3][dim].
 template <class E>
-__global__ __launch_bounds__(kCols * kLanes) void norm_group_sums(NormBackward a, int run, const float* part_sums,
-                                                                  float* group_sums) {
-  __shared__ float sum[kLanes][kCols];
-  const int c = threadIdx.x & (kCols - 1), lane = threadIdx.x / kCols, col = blockIdx.x * kCols + c;
+__global__ __launch_bounds__(64 * kWaves) void norm_group_sums(NormBackward a, int run, int need, const float* part_sums,
+                                                                float* group_sums) {
+  __shared__ ColumnSlots slots;
+  const int share = threadIdx.x / kCols, col = 4 * (int)(blockIdx.x * kCols + threadIdx.x % kCols);
   const bool live = col < a.n.dim;
   const RowGroups& rg = a.n.groups;
   for (int g = blockIdx.y; g < rg.groups; g += gridDim.y) {
     int r0, r1;
     if (rg.starts) {
-      const int limit = group_limit(rg);
-      r0 = rg.starts[g];
-      r1 = rg.starts[g + 1];
+      const int limit = group_limit(rg);  // (the first group starts at 0, the last one ends there)
+      r0 = g == 0 ? 0 : rg.starts[g];
+      r1 = g == rg.groups - 1 ? limit : rg.starts[g + 1];
       r0 = r0 < 0 ? 0 : r0;
       r1 = r1 < limit ? r1 : limit;
     } else {
       r0 = g * rg.per;
       r1 = r0 + rg.per;
     }
-    float s[3] = {0.0f, 0.0f, 0.0f};
+    float4 s[3] = {};
     if (r1 > r0 && live) {
       const int w1 = (r1 - 1) / run;
-      for (int w = r0 / run + lane; w <= w1; w += kLanes) {
+#pragma unroll 4
+      for (int w = r0 / run + share; w <= w1; w += kShares) {
         const float* p = part_sums + (int64_t)(w + g) * 3 * a.n.dim + col;
 #pragma unroll
-        for (int q = 0; q < 3; ++q) s[q] += p[(int64_t)q * a.n.dim];
+        for (int q = 0; q < 3; ++q)
+          if (need >> q & 1) add4(s[q], *reinterpret_cast<const float4*>(p + (int64_t)q * a.n.dim));
       }
     }
-#pragma unroll
-    for (int q = 0; q < 3; ++q) s[q] = column_sum(s[q], sum, c, lane);
-    if (!live || lane != 0) continue;
+    column_sums(s, need, slots);
+    if (!live || share != 0) continue;
+    const int64_t at = (int64_t)g * a.n.dim + col;
     if (a.dscale) {
-      float d = a.n.weight ? s[0] * one<E>(a.n.weight, col) : s[0];
-      if (a.n.bias) d = fmaf(one<E>(a.n.bias, col), s[1], d);
-      a.dscale[(int64_t)g * a.n.dim + col] = d;
+      float4 d = s[0];
+      const float4 zero = make_float4(0, 0, 0, 0);
+      if (a.n.weight) d = fma4(d, four<E>(a.n.weight, col), zero);
+      if (a.n.bias) d = fma4(four<E>(a.n.bias, col), s[1], d);
+      put4(a.dscale, at, d);
     }
-    if (a.dshift) a.dshift[(int64_t)g * a.n.dim + col] = s[1];
-    if (a.dgate)
-      a.dgate[(int64_t)g * a.n.dim + col] = a.n.post_weight ? s[2] * one<E>(a.n.post_weight, col) : s[2];
+    if (a.dshift) put4(a.dshift, at, s[1]);
+    if (a.dgate) put4(a.dgate, at, a.n.post_weight ? fma4(s[2], four<E>(a.n.post_weight, col), make_float4(0, 0, 0, 0)) : s[2]);
     if (group_sums) {
 #pragma unroll
-      for (int q = 0; q < 3; ++q) group_sums[((int64_t)g * 3 + q) * a.n.dim + col] = s[q];
+      for (int q = 0; q < 3; ++q) put4(group_sums, ((int64_t)g * 3 + q) * a.n.dim + col, s[q]);
     } else if (rg.groups == 1) {
-      float t[3] = {0.0f, 0.0f, 0.0f};
+      float4 t[3] = {};
       add_shared<E>(a, g, col, s, t);
       put_shared(a, col, t);
     }
@@ -500,22 +652,22 @@ __global__ __launch_bounds__(kCols * kLanes) void norm_group_sums(NormBackward a
 }
 
 template <class E>
-__global__ __launch_bounds__(kCols * kLanes) void norm_shared_sums(NormBackward a, const float* group_sums) {
-  __shared__ float sum[kLanes][kCols];
-  const int c = threadIdx.x & (kCols - 1), lane = threadIdx.x / kCols, col = blockIdx.x * kCols + c;
+__global__ __launch_bounds__(64 * kWaves) void norm_shared_sums(NormBackward a, const float* group_sums) {
+  __shared__ ColumnSlots slots;
+  const int share = threadIdx.x / kCols, col = 4 * (int)(blockIdx.x * kCols + threadIdx.x % kCols);
   const bool live = col < a.n.dim;
-  float t[3] = {0.0f, 0.0f, 0.0f};
+  float4 t[3] = {};
   if (live) {
-    for (int g = lane; g < a.n.groups.groups; g += kLanes) {
-      float s[3];
+    for (int g = share; g < a.n.groups.groups; g += kShares) {
+      float4 s[3];
 #pragma unroll
-      for (int q = 0; q < 3; ++q) s[q] = group_sums[((int64_t)g * 3 + q) * a.n.dim + col];
+      for (int q = 0; q < 3; ++q)
+        s[q] = *reinterpret_cast<const float4*>(group_sums + ((int64_t)g * 3 + q) * a.n.dim + col);
       add_shared<E>(a, g, col, s, t);
     }
   }
-#pragma unroll
-  for (int q = 0; q < 3; ++q) t[q] = column_sum(t[q], sum, c, lane);
-  if (live && lane == 0) put_shared(a, col, t);
+  column_sums(t, 7, slots);
+  if (live && share == 0) put_shared(a, col, t);
 }
 
 // a call without rows: the gradients of the vectors are sums over nothing
@@ -523,52 +675,57 @@ __global__ __launch_bounds__(256) void zero(float* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
 }
 
+// One chunk a lane up to here in the forward pass, two beyond (8192 x 5120 bf16 into fp8r: 65 us against 77 with one).
+constexpr int kForwardOne = 2048;
+// Waves a compute unit and least rows a worker in the backward pass. 4608 x 2560 bf16: 12 waves 47 us, 8 waves 70, 16 and
+// 20 waves 54 and 65 (workers of five waves do not share out evenly over four SIMDs); a worker of fewer rows writes
+// sums for fewer (1001 x 1536 fp32: 4 rows 24 us, 2 rows 31, 1 row 59).
+constexpr int kBackwardWaves = 12, kBackwardRows = 4;
+
 // ---- launches -----------------------------------------------------------------------
 
-// f(waves of a worker, chunks of a lane): a wave holds rows of up to 1024 elements, four waves up to 8192, eight up to 16384
+// f(whether a worker is one wave, chunks of a lane, whether groups have vectors); waves of a worker
 template <class F>
-hipError_t with_shape(int dim, F f) {
-  using std::integral_constant;
-#define BSQ_SHAPE(W, C) return f(integral_constant<int, W>{}, integral_constant<int, C>{})
-  if (dim <= 512) BSQ_SHAPE(1, 1);
-  if (dim <= 1024) BSQ_SHAPE(1, 2);
-  if (dim <= 2048) BSQ_SHAPE(4, 1);
-  if (dim <= 4096) BSQ_SHAPE(4, 2);
-  if (dim <= 6144) BSQ_SHAPE(4, 3);
-  if (dim <= 8192) BSQ_SHAPE(4, 4);
-  if (dim <= 12288) BSQ_SHAPE(8, 3);
-  BSQ_SHAPE(8, 4);
-#undef BSQ_SHAPE
+hipError_t with_groups(const NormArgs& n, F f) {
+  return n.scale.p || n.shift.p || n.gate.p ? f(std::true_type{}) : f(std::false_type{});
 }
-int waves_of(int64_t dim) { return dim <= 1024 ? 1 : dim <= 8192 ? 4 : 8; }
+template <int C>
+using chunks_t = std::integral_constant<int, C>;
+int waves_of(int64_t dim, int chunks) { return (int)((dim + 512 * chunks - 1) / (512 * chunks)); }
 
 template <class E>
 hipError_t forward(const NormForward& a, hipStream_t s) {
-  return with_shape(a.n.dim, [&](auto w, auto c) {
-    constexpr int W = decltype(w)::value, C = decltype(c)::value, per = workers_of<W>();
-    hipLaunchKernelGGL((block_norm<E, W, C>), dim3((unsigned)((a.n.rows + per - 1) / per)), dim3(threads_of<W>()), 0, s,
-                       a);
+  return with_groups(a.n, [&](auto grouped) {
+    constexpr bool G = decltype(grouped)::value;
+    const unsigned rows = (unsigned)a.n.rows;
+    if (a.n.dim <= 512)
+      hipLaunchKernelGGL((block_norm<E, true, 1, G>), dim3((rows + 3) / 4), dim3(256), 0, s, a);
+    else if (a.n.dim <= kForwardOne)
+      hipLaunchKernelGGL((block_norm<E, false, 1, G>), dim3(rows), dim3(64 * waves_of(a.n.dim, 1)), 0, s, a);
+    else
+      hipLaunchKernelGGL((block_norm<E, false, 2, G>), dim3(rows), dim3(64 * waves_of(a.n.dim, 2)), 0, s, a);
     return hipGetLastError();
   });
 }
 
-// rows of a worker in the backward pass
-int run_of(int64_t rows, int64_t dim) {
-  const int64_t want = dim <= 1024 ? 4096 : 1024;  // workers that fill the 256 compute units
-  const int64_t n = (rows + want - 1) / want;
-  return (int)(n < 4 ? 4 : n);
+int backward_chunks(int64_t dim) { return dim <= 4096 ? 1 : dim <= 8192 ? 2 : 4; }
+// Rows of a worker: so many that the workers fill the 256 compute units once, kBackwardWaves on each, and at least
+// kBackwardRows, since each worker's sums are written once and read once
+int backward_run(int64_t rows, int64_t dim) {
+  const int w = waves_of(dim, backward_chunks(dim));
+  const int64_t workers = 256 * (int64_t)(kBackwardWaves / w > 0 ? kBackwardWaves / w : 1), n = (rows + workers - 1) / workers;
+  return (int)(n < kBackwardRows ? kBackwardRows : n);
 }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t slot_bytes(int64_t rows, int64_t dim, int64_t groups) {
-  const int run = run_of(rows, dim);
+  const int run = backward_run(rows, dim);
   return pad256((size_t)((rows + run - 1) / run + groups) * 3 * (size_t)dim * 4);
 }
 
 template <class E>
 hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
-  const bool shared = a.dweight || a.dbias || a.dpost_weight, vectors = a.dscale || a.dshift || a.dgate || shared;
   if (a.n.rows == 0) {
-    const int64_t all = (int64_t)a.n.groups.groups * a.n.dim;
+    const int64_t all = (int64_t)a.n.groups.end * a.n.dim;
     for (const auto& [p, n] : {std::pair<float*, int64_t>{a.dscale, all}, {a.dshift, all}, {a.dgate, all},
                                {a.dweight, a.n.dim}, {a.dbias, a.n.dim}, {a.dpost_weight, a.n.dim}}) {
       if (!p) continue;
@@ -579,23 +736,34 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
     }
     return hipSuccess;
   }
-  const int run = run_of(a.n.rows, a.n.dim), workers = (a.n.rows + run - 1) / run, groups = a.n.groups.groups;
-  float* parts = vectors ? static_cast<float*>(workspace) : nullptr;
-  hipError_t e = with_shape(a.n.dim, [&](auto w, auto c) {
-    constexpr int W = decltype(w)::value, C = decltype(c)::value, per = workers_of<W>();
-    hipLaunchKernelGGL((block_norm_backward<E, W, C>), dim3((unsigned)((workers + per - 1) / per)),
-                       dim3(threads_of<W>()), 0, s, a, run, parts);
-    return hipGetLastError();
+  const int run = backward_run(a.n.rows, a.n.dim), workers = (a.n.rows + run - 1) / run, groups = a.n.groups.groups;
+  const int need = (a.dscale || a.dweight ? kSumScale : 0) | (a.dshift || a.dbias || (a.dscale && a.n.bias) ? kSumShift : 0) |
+                   (a.dgate || a.dpost_weight ? kSumGate : 0);
+  float* parts = static_cast<float*>(workspace);
+  hipError_t e = with_groups(a.n, [&](auto grouped) {
+    constexpr bool G = decltype(grouped)::value;
+    const int chunks = backward_chunks(a.n.dim);
+    const unsigned threads = a.n.dim <= 512 ? 256u : 64u * waves_of(a.n.dim, chunks);
+    auto go = [&](auto one, auto c) {
+      constexpr bool ONE = decltype(one)::value;
+      hipLaunchKernelGGL((block_norm_backward<E, ONE, decltype(c)::value, G>), dim3(ONE ? (workers + 3) / 4 : workers),
+                         dim3(threads), 0, s, a, run, need, parts);
+      return hipGetLastError();
+    };
+    if (a.n.dim <= 512) return go(std::true_type{}, chunks_t<1>{});
+    if (chunks == 1) return go(std::false_type{}, chunks_t<1>{});
+    if (chunks == 2) return go(std::false_type{}, chunks_t<2>{});
+    return go(std::false_type{}, chunks_t<4>{});
   });
-  if (e != hipSuccess || !vectors) return e;
+  if (e != hipSuccess || !need) return e;
   float* sums = nullptr;
-  if (shared && groups > 1)
+  if ((a.dweight || a.dbias || a.dpost_weight) && groups > 1)
     sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + slot_bytes(a.n.rows, a.n.dim, groups));
-  const unsigned cols = (unsigned)((a.n.dim + kCols - 1) / kCols);
-  hipLaunchKernelGGL(norm_group_sums<E>, dim3(cols, (unsigned)(groups < 65535 ? groups : 65535)), dim3(kCols * kLanes),
-                     0, s, a, run, parts, sums);
+  const unsigned cols = (unsigned)((a.n.dim + 4 * kCols - 1) / (4 * kCols));
+  hipLaunchKernelGGL(norm_group_sums<E>, dim3(cols, (unsigned)(groups < 65535 ? groups : 65535)), dim3(64 * kWaves),
+                     0, s, a, run, need, parts, sums);
   if ((e = hipGetLastError()) != hipSuccess || !sums) return e;
-  hipLaunchKernelGGL(norm_shared_sums<E>, dim3(cols), dim3(kCols * kLanes), 0, s, a, sums);
+  hipLaunchKernelGGL(norm_shared_sums<E>, dim3(cols), dim3(64 * kWaves), 0, s, a, sums);
   return hipGetLastError();
 }
 

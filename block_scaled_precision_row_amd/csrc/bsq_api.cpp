@@ -379,7 +379,8 @@ bsq_status check_epilogue(const bsq_epilogue* p, const uint16_t* y, int64_t ldy,
     if (!aligned(p->gate, 2) || !aligned(p->group_starts, 4)) return BSQ_ERR_ALIGN;
     e.gate = p->gate;
     e.gate_stride = p->gate_stride;
-    e.groups = bsq::RowGroups{p->group_starts, (int)p->groups, (int)(M / p->groups), (int)M};
+    e.groups = bsq::RowGroups{p->group_starts, (int)p->groups, (int)(M / p->groups), (int)M,
+                              (int)p->groups};
   }
   if (p->residual) {
     if (p->residual_stride < N || p->residual_stride >= (int64_t)1 << 40) return BSQ_ERR_SHAPE;
@@ -388,7 +389,6 @@ bsq_status check_epilogue(const bsq_epilogue* p, const uint16_t* y, int64_t ldy,
     e.residual = p->residual;
     e.residual_stride = p->residual_stride;
   }
-  bsq::act_coefficients(e);
   return BSQ_OK;
 }
 }  // namespace

@@ -20,8 +20,9 @@ bsq_status check_groups(int64_t rows, int64_t groups, const int32_t* starts) {
   if (!starts && rows % groups != 0) return BSQ_ERR_SHAPE;
   return aligned(starts, 4) ? BSQ_OK : BSQ_ERR_ALIGN;
 }
-bsq::RowGroups groups_of(int64_t rows, int64_t groups, const int32_t* starts) {
-  return bsq::RowGroups{starts, (int)groups, (int)(rows / groups), (int)rows};
+bsq::RowGroups groups_of(int64_t rows, int64_t groups, const int32_t* starts, bool vectors) {
+  if (!vectors) return bsq::RowGroups{starts, 1, (int)rows, (int)rows, (int)groups};
+  return bsq::RowGroups{starts, (int)groups, (int)(rows / groups), (int)rows, (int)groups};
 }
 
 // ---- block norms ---------------------------------------------------------------------
@@ -55,7 +56,7 @@ bsq::NormArgs norm_args(const bsq_block* b) {
   bsq::NormArgs n{};
   n.norm = b->norm; n.post = b->post; n.eps = b->eps; n.post_eps = b->post_eps;
   n.rows = (int)b->rows; n.dim = (int)b->dim;
-  n.groups = groups_of(b->rows, b->groups, b->group_starts);
+  n.groups = groups_of(b->rows, b->groups, b->group_starts, b->scale || b->shift || b->gate);
   n.weight = b->weight; n.bias = b->bias; n.post_weight = b->post_weight;
   n.scale = bsq::GroupVector{b->scale, b->scale_stride};
   n.shift = bsq::GroupVector{b->shift, b->shift_stride};

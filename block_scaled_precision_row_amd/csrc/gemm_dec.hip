@@ -286,9 +286,12 @@ __device__ __forceinline__ void dec_tile(const DecArgs& a, const Finish& finish)
   if constexpr (!std::is_same<Finish, gemm::NoFinish>::value) {  // (every wave has passed the last stage's barrier)
     constexpr int TROW = BN * 2 + 16;
     static_assert(MODE == kW4A4 && !LORA && BM * TROW <= 2 * STAGE, "the output tile fits the stage buffers");
-    auto scaled = [&](int i, int j, int g) {
+    auto scaled = [&](int i, int j, int g, const float4* bias) {
       const v16f& A = acc[i][j];
-      return make_float4(A[4 * g + 0] * alpha, A[4 * g + 1] * alpha, A[4 * g + 2] * alpha, A[4 * g + 3] * alpha);
+      if (!bias) return make_float4(A[4 * g] * alpha, A[4 * g + 1] * alpha, A[4 * g + 2] * alpha, A[4 * g + 3] * alpha);
+      const float4 b = *bias;
+      return make_float4(fmaf(A[4 * g], alpha, b.x), fmaf(A[4 * g + 1], alpha, b.y), fmaf(A[4 * g + 2], alpha, b.z),
+                         fmaf(A[4 * g + 3], alpha, b.w));
     };
     finish.template tile<BM, BN, TROW, TN, TM>(smem, a.y, a.ldy, M, N, m0, n0, wm * WM, wn * WN, tid, false, scaled);
     return;

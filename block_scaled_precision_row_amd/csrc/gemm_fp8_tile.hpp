@@ -424,12 +424,15 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
   __syncthreads();  // all stage buffers are free now
   if constexpr (kFinish) {
     static_assert(!LORA && OQ == 0, "the epilogue's linears have neither an adapter nor a quantized output");
-    auto scaled = [&](int i, int j, int g) {
+    auto scaled = [&](int i, int j, int g, const float4* bias) {
       const v16f& A = acc[i][j];
       const float xs = s_sx[wm * C::WM + j * 32 + lr];
       const float4 s4 = *reinterpret_cast<const float4*>(&s_sw[wn * C::WN + i * 32 + 8 * g + 4 * lh]);
-      return make_float4(A[4 * g + 0] * xs * s4.x, A[4 * g + 1] * xs * s4.y, A[4 * g + 2] * xs * s4.z,
-                         A[4 * g + 3] * xs * s4.w);
+      if (!bias)
+        return make_float4(A[4 * g] * xs * s4.x, A[4 * g + 1] * xs * s4.y, A[4 * g + 2] * xs * s4.z, A[4 * g + 3] * xs * s4.w);
+      const float4 b = *bias;
+      return make_float4(fmaf(A[4 * g] * xs, s4.x, b.x), fmaf(A[4 * g + 1] * xs, s4.y, b.y),
+                         fmaf(A[4 * g + 2] * xs, s4.z, b.z), fmaf(A[4 * g + 3] * xs, s4.w, b.w));
     };
     finish.template tile<BM, BN, C::TROW, TN, TM>(smem, y, ldy, M, N, m0, n0, wm * C::WM, wn * C::WN, tid,
                                                   stream_y != 0, scaled);

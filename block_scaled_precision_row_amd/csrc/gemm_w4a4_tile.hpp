@@ -290,9 +290,12 @@ __device__ __forceinline__ void w4a4_tile(const DecArgs& a, int bid, const Finis
     static_assert(!LORA, "an adapter's linear has no epilogue");
     __syncthreads();  // no stage buffer is read any more
     const float alpha = s_g[0][0] * s_g[1][0];
-    auto scaled = [&](int i, int j, int g) {
+    auto scaled = [&](int i, int j, int g, const float4* bias) {
       const v16f& A = acc[i][j];
-      return make_float4(A[4 * g + 0] * alpha, A[4 * g + 1] * alpha, A[4 * g + 2] * alpha, A[4 * g + 3] * alpha);
+      if (!bias) return make_float4(A[4 * g] * alpha, A[4 * g + 1] * alpha, A[4 * g + 2] * alpha, A[4 * g + 3] * alpha);
+      const float4 b = *bias;
+      return make_float4(fmaf(A[4 * g], alpha, b.x), fmaf(A[4 * g + 1], alpha, b.y), fmaf(A[4 * g + 2], alpha, b.z),
+                         fmaf(A[4 * g + 3], alpha, b.w));
     };
     finish.template tile<BM, BN, C::TROW, TN, TM>(smem, a.y, a.ldy, M, N, m0, n0, wm * C::WM, wn * C::WN, tid,
                                                   a.stream_y != 0, scaled);

@@ -11,12 +11,13 @@ struct RowGroups {
   int groups;
   int per;
   int rows;  // of the call
+  int end;   // starts[end] ends the last group (a call without vectors of groups counts all its rows as one's)
 };
 
 // rows of groups: from here on a row is not written
 __device__ __forceinline__ int group_limit(const RowGroups& r) {
   if (!r.starts) return r.rows;
-  const int n = r.starts[r.groups];
+  const int n = r.starts[r.end];
   return n < 0 ? 0 : (n < r.rows ? n : r.rows);
 }
 
@@ -34,6 +35,12 @@ __device__ __forceinline__ int group_of_wave(const RowGroups& r, int row, int la
     n = n - k * step < step ? n - k * step : step;
   }
   return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// the first row behind group g
+__device__ __forceinline__ int group_end(const RowGroups& r, int g) {
+  if (!r.starts) return (g + 1) * r.per;
+  return r.starts[g + 1];
 }
 
 // the group of each lane's own row, which lies between those of two rows whose groups are first and last

@@ -125,7 +125,8 @@ def test_forward_encoded(T, D, norm, post, groups, starts, want, kind):
 @pytest.mark.parametrize("T,D,norm,post,groups,starts,want", CASES + [
     (9, 64, None, "rms", 2, [0, 4, 8], dict(branch=1, gate=1, post_weight=1)),
     (40, 2560, None, None, 2, None, dict(branch=1, gate=1)),
-    (5000, 64, "rms", "rms", 2, [0, 4999, 5000], ALL)])
+    (5000, 64, "rms", "rms", 2, [0, 4999, 5000], ALL), (2000, 4096, "layer", None, 1, None, dict(weight=1, bias=1)),
+    (700, 4608, "layer", "rms", 7, None, ALL)])
 def test_backward(T, D, norm, post, groups, starts, want, kind):
     v = vectors(T + D + 2, T, D, kind, groups, strided=T % 2 == 0, **want)
     group, st = groups_of(T, groups, starts)
@@ -343,3 +344,27 @@ def test_offsets_past_32_bits():
     assert torch.equal(got[0], want[0]) and torch.equal(x, want[2])
     dx = L.bsq_block_norm_backward(v, None, x, need=("x",), dx=x)["x"]
     assert torch.equal(dx, L.bsq_block_norm_backward(v, None, want[2], need=("x",))["x"])
+
+
+@pytest.mark.parametrize("D", [64, 1032, 4104])
+def test_starts_without_vectors(D):
+    """Where only starts are given, rows behind the last group are still left alone and reach no sum."""
+    T = 50
+    v = vectors(9, T, D, "bf16", 1, branch=1, weight=1, bias=1)
+    st = torch.tensor([0, 7, 7, 41], dtype=torch.int32).cuda()
+    pad = torch.full((3, T, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    y, _, x = L.bsq_block_norm(norm=L.BSQ_NORM_LAYER, starts=st, y=pad[0], x_out=pad[1], **v)
+    part = {k: t[:41] if k in ("x", "branch") and t is not None else t for k, t in v.items()}
+    want = L.bsq_block_norm(norm=L.BSQ_NORM_LAYER, **part)
+    assert torch.equal(y[:41], want[0]) and torch.equal(x[:41], want[2]) and torch.all(pad[:2, 41:] == 7.0)
+    dy = torch.randn(T, D, device="cuda").bfloat16()
+    dy[41:] = float("nan")
+    back = {k: t for k, t in v.items() if k != "x"}
+    got = L.bsq_block_norm_backward(dy, None, x, norm=L.BSQ_NORM_LAYER, starts=st, dx=pad[2], **back)
+    group = np.where(np.arange(T) < 41, 0, -1)
+    clean = np.nan_to_num(f64(dy))
+    ref, tol = backward_bounds(clean, None, f64(x), "layer", EPS, group, 1, **doubles(back))
+    for k in ("weight", "bias"):
+        assert np.all(np.abs(f64(got[k]) - ref[k]) <= tol[k] + 2.0 ** -23 * np.abs(ref[k])), k
+    assert torch.all(pad[2, 41:] == 7.0)
+    assert np.all(np.abs(f64(got["x"]) - ref["x"])[:41] <= (tol["x"] + rounded(ref["x"], torch.bfloat16))[:41])
