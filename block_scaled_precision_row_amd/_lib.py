@@ -819,7 +819,8 @@ def bsq_rope_axes(x, positions, inv_freq, sections, order=BSQ_AXES_BLOCKS, layou
     else:
         yt, yh = _heads_like(y, shape, dtype, dev, "y")
     axes = len(sections)
-    _like(positions, (T, axes), torch.int64, dev, "positions")
+    if positions.dtype is not torch.int64 or positions.shape != (T, axes) or positions.get_device() != dev.index:
+        _like(positions, (T, axes), torch.int64, dev, "positions")
     pt, pa = positions.stride()
     freq = _flat(inv_freq, (sum(sections),), torch.float32, dev, "inv_freq")
     _call("bsq_rope_axes", dev, _DTYPES[dtype], x.data_ptr(), xt, xh, positions.data_ptr(), pt, pa,
@@ -858,17 +859,26 @@ def _block(x, norm, eps, weight, bias, scale, shift, gate, post, post_weight, po
     """The descriptor of a block's norms for rows like x: (Block, its shape)."""
     if x is None or x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda:
         raise ValueError("rows must be 2-D tensors of bfloat16, float16 or float32 on the GPU")
-    shape, dtype, dev = x.shape, x.dtype, x.device
-    rows, dim = shape
-    groups = _group_count((scale, shift, gate), starts)
-    w, b, pw = (None if v is None else _flat(v, (dim,), dtype, dev, name)
-                for v, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight")))
-    like = (groups, dim)
-    sc, scs = _row_stride(scale, like, dtype, dev, "scale")
-    sh, shs = _row_stride(shift, like, dtype, dev, "shift")
-    ga, gas = _row_stride(gate, like, dtype, dev, "gate")
+    dtype, dev = x.dtype, x.device
+    rows, dim = x.shape
+    w = b = pw = sc = sh = ga = None
+    scs = shs = gas = 0
+    if weight is not None:
+        w = _flat(weight, (dim,), dtype, dev, "weight")
+    if bias is not None:
+        b = _flat(bias, (dim,), dtype, dev, "bias")
+    if post_weight is not None:
+        pw = _flat(post_weight, (dim,), dtype, dev, "post_weight")
+    if scale is None and shift is None and gate is None:
+        groups = 1 if starts is None else starts.shape[0] - 1
+    else:
+        groups = _group_count((scale, shift, gate), starts)
+        like = (groups, dim)
+        sc, scs = _row_stride(scale, like, dtype, dev, "scale")
+        sh, shs = _row_stride(shift, like, dtype, dev, "shift")
+        ga, gas = _row_stride(gate, like, dtype, dev, "gate")
     return Block(_DTYPES[dtype], norm, post, eps, eps if post_eps is None else post_eps, rows, dim, groups,
-                 _starts_of(starts, groups, dev), w, b, pw, sc, sh, ga, scs, shs, gas)
+                 None if starts is None else _starts_of(starts, groups, dev), w, b, pw, sc, sh, ga, scs, shs, gas)
 
 
 def bsq_block_norm(x, norm=BSQ_NORM_RMS, eps=1e-6, weight=None, bias=None, scale=None, shift=None, branch=None,
@@ -883,12 +893,14 @@ def bsq_block_norm(x, norm=BSQ_NORM_RMS, eps=1e-6, weight=None, bias=None, scale
     shape, dtype, dev = x.shape, x.dtype, x.device
     T, D = shape
     xp, xs = _row_stride(x, shape, dtype, dev, "x")
-    bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
-    if branch is not None and x_out is None:
-        x_out = torch.empty(shape, dtype=dtype, device=dev)
-    op, os_ = _row_stride(x_out, shape, dtype, dev, "x_out")
-    yp = ysp = None
-    ys = 0
+    bp = op = yp = ysp = None
+    bs = os_ = ys = 0
+    if branch is not None:
+        bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
+        if x_out is None:
+            x_out = torch.empty(shape, dtype=dtype, device=dev)
+    if x_out is not None:
+        op, os_ = _row_stride(x_out, shape, dtype, dev, "x_out")
     if out_format is None:
         if norm != BSQ_NORM_NONE:
             if y is None:
@@ -928,53 +940,68 @@ def bsq_block_norm_backward(dy, dx_out, x_out, norm=BSQ_NORM_RMS, eps=1e-6, weig
     shape, dtype, dev = like.shape, like.dtype, like.device
     T, D = shape
     groups = block.groups
-
-    def asked(name):
-        return need is None or name in need
-
-    yp, ys = _row_stride(dy, shape, dtype, dev, "dy")
-    dp, ds = _row_stride(dx_out, shape, dtype, dev, "dx_out")
-    op, os_ = _row_stride(x_out, shape, dtype, dev, "x_out")
-    bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
-    own_branch = branch is not None and asked("branch") and (gate is not None or post != BSQ_NORM_NONE)
-    if dx is None and (asked("x") or (branch is not None and asked("branch") and not own_branch)):
+    yp = dp = op = bp = xp = hp = None
+    ys = ds = os_ = bs = xs = hs = 0
+    if dy is not None:
+        yp, ys = _row_stride(dy, shape, dtype, dev, "dy")
+        op, os_ = _row_stride(x_out, shape, dtype, dev, "x_out")
+    if dx_out is not None:
+        dp, ds = _row_stride(dx_out, shape, dtype, dev, "dx_out")
+    of_branch = branch is not None and (need is None or "branch" in need)
+    own = of_branch and (gate is not None or post != BSQ_NORM_NONE)
+    if branch is not None:
+        bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
+    if dx is None and (need is None or "x" in need or (of_branch and not own)):
         dx = torch.empty(shape, dtype=dtype, device=dev)
-    if dbranch is None and own_branch:
+    if dbranch is None and own:
         dbranch = torch.empty(shape, dtype=dtype, device=dev)
-    xp, xs = _row_stride(dx, shape, dtype, dev, "dx")
-    hp, hs = _row_stride(dbranch, shape, dtype, dev, "dbranch")
-
-    def grad(vector, name, size):
-        return torch.empty(size, dtype=torch.float32, device=dev) if vector is not None and asked(name) else None
-
-    out = {"x": dx, "branch": dbranch if dbranch is not None or branch is None or not asked("branch") else dx,
-           "gate": grad(gate, "gate", (groups, D)), "scale": grad(scale, "scale", (groups, D)),
-           "shift": grad(shift, "shift", (groups, D)), "weight": grad(weight, "weight", (D,)),
-           "bias": grad(bias, "bias", (D,)), "post_weight": grad(post_weight, "post_weight", (D,))}
-    vectors = [None if out[k] is None else out[k].data_ptr()
-               for k in ("scale", "shift", "gate", "weight", "bias", "post_weight")]
+    if dx is not None:
+        xp, xs = _row_stride(dx, shape, dtype, dev, "dx")
+    if dbranch is not None:
+        hp, hs = _row_stride(dbranch, shape, dtype, dev, "dbranch")
+    out = {"x": dx, "branch": dbranch if dbranch is not None or not of_branch else dx}
+    pointers = {}
+    for name, vector, size in (("scale", scale, (groups, D)), ("shift", shift, (groups, D)), ("gate", gate, (groups, D)),
+                               ("weight", weight, (D,)), ("bias", bias, (D,)), ("post_weight", post_weight, (D,))):
+        t = p = None
+        if vector is not None and (need is None or name in need):
+            t = torch.empty(size, dtype=torch.float32, device=dev)
+            p = t.data_ptr()
+        out[name], pointers[name] = t, p
+    n = 0
     if workspace is None:
-        if any(v is not None for v in vectors) and T:
-            workspace = torch.empty((lib.bsq_block_norm_workspace_bytes(T, D, groups),), dtype=torch.uint8, device=dev)
+        if T and any(pointers.values()):
+            n = lib.bsq_block_norm_workspace_bytes(T, D, groups)
+            workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev:
         raise ValueError("workspace must be on %s" % dev)
-    _call("bsq_block_norm_backward", dev, block, yp, ys, dp, ds, op, os_, bp, bs, xp, xs, hp, hs, *vectors,
-          None if workspace is None else workspace.data_ptr(), _nbytes(workspace))
+    else:
+        n = _nbytes(workspace)
+    _call("bsq_block_norm_backward", dev, block, yp, ys, dp, ds, op, os_, bp, bs, xp, xs, hp, hs, *pointers.values(),
+          None if workspace is None else workspace.data_ptr(), n)
     return out
 
 
 def _epilogue(M, N, bias, act, gate, residual, starts, y, dev):
     """The descriptor of an epilogue, y and its leading dimension."""
     bf16 = torch.bfloat16
-    groups = _group_count((gate,), starts)
-    bp = None if bias is None else _flat(bias, (N,), bf16, dev, "bias")
-    gp, gs = _row_stride(gate, (groups, N), bf16, dev, "gate")
-    rp, rs = _row_stride(residual, (M, N), bf16, dev, "residual")
+    shape, groups = (M, N), 1
+    bp = gp = rp = None
+    gs = rs = 0
+    if bias is not None:
+        bp = _flat(bias, (N,), bf16, dev, "bias")
+    if gate is not None:
+        groups = _group_count((gate,), starts)
+        gp, gs = _row_stride(gate, (groups, N), bf16, dev, "gate")
+        starts = _starts_of(starts, groups, dev)
+    elif starts is not None:
+        raise ValueError("starts without a gate")
+    if residual is not None:
+        rp, rs = _row_stride(residual, shape, bf16, dev, "residual")
     if y is None:
-        y = torch.empty((M, N), dtype=bf16, device=dev)
-    yp, ys = _row_stride(y, (M, N), bf16, dev, "y")
-    return Epilogue(act, bp, gp, gs, rp, rs if M > 1 else N, groups, _starts_of(starts, groups, dev)), y, yp, (
-        ys if M > 1 else N)
+        y = torch.empty(shape, dtype=bf16, device=dev)
+    yp, ys = _row_stride(y, shape, bf16, dev, "y")
+    return Epilogue(act, bp, gp, gs, rp, rs if M > 1 else N, groups, starts), y, yp, (ys if M > 1 else N)
 
 
 def bsq_gemm_fp8r_q_epilogue(xq, x_scale, w, w_scale, bias=None, act=BSQ_ACT_NONE, gate=None, residual=None, starts=None,

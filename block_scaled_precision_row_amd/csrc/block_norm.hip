@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 // Sums (or the maximum) over the waves of a worker: over the lanes, then through LDS, where each reduction of a row has
 // room of its own and rows alternate between two sets of it: a wave that is a row ahead has passed a barrier that the
 // others reach only after they have read the set before. ONE: the worker is one wave.
-constexpr int kReductions = 6, kMostSums = 2;  // of a row at most: two norms of two each, and one for each gradient
+constexpr int kReductions = 5, kMostSums = 4;  // of a row at most (forward: two norms of two each, and the maximum)
 constexpr int kMostWaves = 16;
 struct Slots {
   float s[2][kReductions][kMostSums][kMostWaves];
@@ -372,9 +372,12 @@ __global__ __launch_bounds__(most_threads<ONE>()) void block_norm(NormForward a)
 
 enum { kSumScale = 1, kSumShift = 2, kSumGate = 4 };  // which of the three sums a call needs
 
-template <class E, bool ONE, int C, bool GROUPED>
+// A row's tensors stay as they are in memory and are taken to fp32 again in each of its passes: (A) the means, (B) the
+// sizes and, with them, the sums along the gradient, (C) the gradients; with a post norm also (D) the sums along the
+// branch's. The next row's loads are under way meanwhile.
+template <class E, bool ONE, int C, bool GROUPED, bool POST>
 __global__ __launch_bounds__(ONE ? 256 : kBackwardThreads) void block_norm_backward(NormBackward a, int run, int need,
-                                                                           float* part_sums) {
+                                                                                    float* part_sums) {
   typedef typename E::elem elem;
   __shared__ Slots slots;
   const NormArgs& n = a.n;
@@ -384,7 +387,7 @@ __global__ __launch_bounds__(ONE ? 256 : kBackwardThreads) void block_norm_backw
   if (first >= last) return;  // (the whole worker)
   const float inv_dim = 1.0f / (float)n.dim;
   const bool layer = n.norm == BSQ_NORM_LAYER, post_layer = n.post == BSQ_NORM_LAYER;
-  const bool normed = n.norm != BSQ_NORM_NONE, post = n.post != BSQ_NORM_NONE, branch = a.branch.p != nullptr;
+  const bool normed = n.norm != BSQ_NORM_NONE;
   float sums[3][C][8];
 #pragma unroll
   for (int k = 0; k < C; ++k)
@@ -401,17 +404,19 @@ __global__ __launch_bounds__(ONE ? 256 : kBackwardThreads) void block_norm_backw
         for (int e = 0; e < 8; ++e) sums[q][k][e] = 0.0f;
       }
   };
-  constexpr bool kAhead = C <= 2;  // the next row's loads, while registers allow it
-  Chunk<E> x[C], dy[C], dx[C], h[C];
-  Vector<E, C, C <= 2 && !GROUPED> weight, pw;
-  Vector<E, C, C <= 2 && GROUPED> scale, gate;
-  auto load_row = [&](int row) {
-    me.load(x, normed ? row_of<E>(a.x_out, row) : nullptr);
-    me.load(dy, normed ? row_of<E>(a.dy, row) : nullptr);
-    me.load(h, row_of<E>(a.branch, row));
-    me.load(dx, row_of<E>(a.dx_out, row));
+  constexpr bool kHold = C * sizeof(elem) <= 8, kAhead = kHold && (!POST || C == 1);  // (as registers allow)
+  struct Row {
+    Chunk<E> x[C], dy[C], dx[C], h[C];
+  } now, next;
+  auto load_row = [&](Row& r, int row) {
+    me.load(r.x, normed ? row_of<E>(a.x_out, row) : nullptr);
+    me.load(r.dy, normed ? row_of<E>(a.dy, row) : nullptr);
+    me.load(r.h, row_of<E>(a.branch, row));
+    me.load(r.dx, row_of<E>(a.dx_out, row));
   };
-  load_row(first);
+  Vector<E, C, kHold && !GROUPED> weight, pw;
+  Vector<E, C, kHold && GROUPED> scale, gate;
+  if constexpr (kAhead) load_row(next, first);
   weight.set(me, row_of<E>(n.weight));
   pw.set(me, row_of<E>(n.post_weight));
   int g = GROUPED ? -1 : 0, end = first;  // (without vectors of groups all rows count as one's)
@@ -423,111 +428,150 @@ __global__ __launch_bounds__(ONE ? 256 : kBackwardThreads) void block_norm_backw
       scale.set(me, row_of<E>(n.scale, g));
       gate.set(me, row_of<E>(n.gate, g));
     }
-    if (!kAhead && row > first) load_row(row);
+    if constexpr (kAhead) {
+      now = next;
+      if (row + 1 < last) load_row(next, row + 1);
+    } else {
+      load_row(now, row);
+    }
     RowSums<ONE> rs{&slots, me.part, me.parts, me.lane, row, 0};
-    float c[C][8], v[C][8], d[C][8], f[C][8];
+    // dy (1 + scale) weight of chunk k
+    auto scaled = [&](int k, const float (&dy)[8], float (&d)[8]) {
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      dx[k].get(c[k]);
-      x[k].get(v[k]);
-      dy[k].get(d[k]);
-      h[k].get(f[k]);
-    }
-    if (kAhead && row + 1 < last) load_row(row + 1);
-    float hr = 1.0f, r = 0.0f, along = 0.0f, mean = 0.0f;
-    if (branch && post) {
-      hr = size_of<ONE, C>(f, post_layer, n.post_eps, inv_dim, me.has, rs);
+      for (int e = 0; e < 8; ++e) d[e] = dy[e];
+      float w[8];
+      if (GROUPED && scale.p) {
+        scale.get(me, k, w);
 #pragma unroll
-      for (int k = 0; k < C; ++k)
+        for (int e = 0; e < 8; ++e) d[e] = fmaf(d[e], w[e], d[e]);
+      }
+      if (weight.p) {
+        weight.get(me, k, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[k][e] *= hr;
-    }
-    if (normed) {
-      r = size_of<ONE, C>(v, layer, n.eps, inv_dim, me.has, rs);
-      float s[2] = {0.0f, 0.0f};
+        for (int e = 0; e < 8; ++e) d[e] *= w[e];
+      }
+    };
+    // A
+    float mean = 0.0f, post_mean = 0.0f;
+    if (layer || (POST && post_layer)) {
+      float t[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < C; ++k) {
+        float f[8];
+        if (layer) {
+          now.x[k].get(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= r;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sums[0][k][e] = fmaf(d[k][e], v[k][e], sums[0][k][e]);
-          sums[1][k][e] += d[k][e];
+          for (int e = 0; e < 8; ++e) t[0] += f[e];
         }
-        float w[8];
-        if (GROUPED && scale.p) {
-          scale.get(me, k, w);
+        if (POST && post_layer) {
+          now.h[k].get(f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[k][e] = fmaf(d[k][e], w[e], d[k][e]);
-        }
-        if (weight.p) {
-          weight.get(me, k, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[k][e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[0] = fmaf(d[k][e], v[k][e], s[0]);
-          s[1] += d[k][e];
+          for (int e = 0; e < 8; ++e) t[1] += f[e];
         }
       }
-      rs.sum(s);
-      along = s[0] * inv_dim;
-      mean = layer ? s[1] * inv_dim : 0.0f;
+      rs.sum(t);
+      mean = t[0] * inv_dim;
+      post_mean = t[1] * inv_dim;
     }
+    // B
+    float r = 0.0f, along = 0.0f, level = 0.0f, hr = 1.0f;
+    if (normed || POST) {
+      float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        if (!me.has[k]) continue;
+        float f[8], d[8];
+        if (normed) {
+          now.x[k].get(f);
+          float dy[8];
+          now.dy[k].get(dy);
+          scaled(k, dy, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = f[e] - mean;
+            t[0] = fmaf(v, v, t[0]);
+            t[1] = fmaf(d[e], v, t[1]);
+            t[2] += d[e];
+          }
+        }
+        if constexpr (POST) {
+          now.h[k].get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = f[e] - post_mean;
+            t[3] = fmaf(v, v, t[3]);
+          }
+        }
+      }
+      rs.sum(t);
+      r = normed ? 1.0f / sqrtf(t[0] * inv_dim + n.eps) : 0.0f;
+      along = t[1] * r * inv_dim;
+      level = layer ? t[2] * inv_dim : 0.0f;
+      if constexpr (POST) hr = 1.0f / sqrtf(t[3] * inv_dim + n.post_eps);
+    }
+    // C
+    float o[POST ? C : 1][8], hn[POST ? C : 1][8];
+    float t[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < C; ++k) {
+      if (!me.has[k]) continue;
+      float c[8], f[8], w[8];
+      now.dx[k].get(c);
       if (normed) {
+        float dy[8], d[8];
+        now.x[k].get(f);
+        now.dy[k].get(dy);
+        scaled(k, dy, d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] = fmaf(r, d[k][e] - mean - v[k][e] * along, c[k][e]);
+        for (int e = 0; e < 8; ++e) {
+          const float v = (f[e] - mean) * r;
+          c[e] = fmaf(r, fmaf(-v, along, d[e] - level), c[e]);
+          sums[0][k][e] = fmaf(dy[e], v, sums[0][k][e]);
+          sums[1][k][e] += dy[e];
+        }
       }
-    }
+      if (a.dx.p) store8<E>(out_of<E>(a.dx, row) + me.at[k], c);
+      now.h[k].get(f);  // (0 without a branch)
+      if constexpr (POST) {
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      if (!me.has[k]) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] = 0.0f;
+        for (int e = 0; e < 8; ++e) hn[k][e] = f[e] = (f[e] - post_mean) * hr;
       }
-      if (a.dx.p && me.has[k]) store8<E>(out_of<E>(a.dx, row) + me.at[k], c[k]);
-      if (branch) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[2][k][e] = fmaf(c[k][e], f[k][e], sums[2][k][e]);
-      }
-    }
-    if (!a.dbranch.p) continue;
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      float w[8];
+      for (int e = 0; e < 8; ++e) sums[2][k][e] = fmaf(c[e], f[e], sums[2][k][e]);
+      if (!a.dbranch.p) continue;
       if (GROUPED && gate.p) {
         gate.get(me, k, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] *= w[e];
+        for (int e = 0; e < 8; ++e) c[e] *= w[e];
       }
-      if (post) {
+      if constexpr (POST) {
         if (pw.p) {
           pw.get(me, k, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) c[k][e] *= w[e];
+          for (int e = 0; e < 8; ++e) c[e] *= w[e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s[0] = fmaf(c[k][e], f[k][e], s[0]);
-          s[1] += c[k][e];
+          o[k][e] = c[e];
+          t[0] = fmaf(c[e], f[e], t[0]);
+          t[1] += c[e];
         }
+      } else {
+        store8<E>(out_of<E>(a.dbranch, row) + me.at[k], c);
       }
     }
-    if (post) {
-      rs.sum(s);
-      const float along = s[0] * inv_dim, mean = post_layer ? s[1] * inv_dim : 0.0f;
+    // D
+    if (POST && a.dbranch.p) {
+      rs.sum(t);
+      const float post_along = t[0] * inv_dim, post_level = post_layer ? t[1] * inv_dim : 0.0f;
 #pragma unroll
-      for (int k = 0; k < C; ++k)
+      for (int k = 0; k < (POST ? C : 0); ++k) {
+        if (!me.has[k]) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[k][e] = hr * (c[k][e] - mean - f[k][e] * along);
+        for (int e = 0; e < 8; ++e) o[k][e] = hr * fmaf(-hn[k][e], post_along, o[k][e] - post_level);
+        store8<E>(out_of<E>(a.dbranch, row) + me.at[k], o[k]);
+      }
     }
-#pragma unroll
-    for (int k = 0; k < C; ++k)
-      if (me.has[k]) store8<E>(out_of<E>(a.dbranch, row) + me.at[k], c[k]);
   }
   if (need) flush(g);
 }
@@ -708,7 +752,7 @@ hipError_t forward(const NormForward& a, hipStream_t s) {
   });
 }
 
-int backward_chunks(int64_t dim) { return dim <= 4096 ? 1 : dim <= 8192 ? 2 : 4; }
+int backward_chunks(int64_t dim) { return dim <= 4096 ? 1 : dim <= 8192 ? 2 : dim <= 12288 ? 3 : 4; }
 // Rows of a worker: so many that the workers fill the 256 compute units once, kBackwardWaves on each, and at least
 // kBackwardRows, since each worker's sums are written once and read once
 int backward_run(int64_t rows, int64_t dim) {
@@ -743,16 +787,21 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
   hipError_t e = with_groups(a.n, [&](auto grouped) {
     constexpr bool G = decltype(grouped)::value;
     const int chunks = backward_chunks(a.n.dim);
-    const unsigned threads = a.n.dim <= 512 ? 256u : 64u * waves_of(a.n.dim, chunks);
-    auto go = [&](auto one, auto c) {
-      constexpr bool ONE = decltype(one)::value;
-      hipLaunchKernelGGL((block_norm_backward<E, ONE, decltype(c)::value, G>), dim3(ONE ? (workers + 3) / 4 : workers),
-                         dim3(threads), 0, s, a, run, need, parts);
+    const bool one = a.n.dim <= 512;
+    const unsigned blocks = one ? (workers + 3) / 4 : workers, threads = one ? 256u : 64u * waves_of(a.n.dim, chunks);
+    auto go = [&](auto o, auto c) {
+      constexpr bool ONE = decltype(o)::value;
+      constexpr int C = decltype(c)::value;
+      if (a.branch.p && a.n.post != BSQ_NORM_NONE)
+        hipLaunchKernelGGL((block_norm_backward<E, ONE, C, G, true>), dim3(blocks), dim3(threads), 0, s, a, run, need, parts);
+      else
+        hipLaunchKernelGGL((block_norm_backward<E, ONE, C, G, false>), dim3(blocks), dim3(threads), 0, s, a, run, need, parts);
       return hipGetLastError();
     };
-    if (a.n.dim <= 512) return go(std::true_type{}, chunks_t<1>{});
+    if (one) return go(std::true_type{}, chunks_t<1>{});
     if (chunks == 1) return go(std::false_type{}, chunks_t<1>{});
     if (chunks == 2) return go(std::false_type{}, chunks_t<2>{});
+    if (chunks == 3) return go(std::false_type{}, chunks_t<3>{});
     return go(std::false_type{}, chunks_t<4>{});
   });
   if (e != hipSuccess || !need) return e;

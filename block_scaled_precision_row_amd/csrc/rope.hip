@@ -2,7 +2,7 @@
 //
 // Bound by memory: every element is read and written once; an angle costs some 55 instructions
 // and serves all heads of its token, so a workgroup first puts the cosines and sines of its tokens
-// into LDS and then streams the tokens' heads, 16 elements (eight pairs) a thread and step. 8192 tokens of
+// into LDS and then streams the tokens' heads, 16 bytes of each half of eight pairs (four of fp32) a thread and step. 8192 tokens of
 // 40 heads of 128, fp16: 168 MB in 32.8 us, 5.1 TB/s, what a copy reaches; 48 tokens of 40 heads 3.1 us, a launch.
 //
 // With several axes (bsq_rope_axes) the angles take their pair's axis' position, and nothing else changes: 14400 tokens
@@ -52,7 +52,24 @@ struct Axes {
   }
 };
 
-// eight pairs per thread and step: rot % 16 == 0, D % 16 == 0, 16-byte accesses
+// P pairs per thread and step, in two 16-byte accesses: eight pairs, four of fp32 (with eight, whose lanes are 64 bytes
+// apart, the fp32 gradient of 5001 x 24 x 128 took 32 us); rot % 16 == 0, D % 16 == 0
+template <class E>
+constexpr int pairs_of() { return sizeof(typename E::elem) == 4 ? 4 : 8; }
+template <class E>
+__device__ __forceinline__ void load_step(const typename E::elem* p, float (&f)[pairs_of<E>()]) { load8<E>(p, f); }
+template <>
+__device__ __forceinline__ void load_step<Fp32>(const float* p, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+template <class E>
+__device__ __forceinline__ void store_step(typename E::elem* p, const float (&f)[pairs_of<E>()]) { store8<E>(p, f); }
+template <>
+__device__ __forceinline__ void store_step<Fp32>(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+
 template <class E, bool INTER, bool BACK, class X>
 __global__ __launch_bounds__(256) void rope_vec(RopeArgs a, X axes) {
   extern __shared__ float2 cs[];  // [tokens][rot / 2]
@@ -69,24 +86,25 @@ __global__ __launch_bounds__(256) void rope_vec(RopeArgs a, X axes) {
     cs[i] = v;
   }
   __syncthreads();
-  const int units = a.D >> 4;  // 16 elements each
+  constexpr int P = pairs_of<E>();
+  const int units = a.D / (2 * P);
   const int per_token = nh * units;
   for (int i = threadIdx.x; i < nt * per_token; i += 256) {
     const int t = i / per_token, r = i - t * per_token, h = r / units, u = r - h * units;
     const elem* x = static_cast<const elem*>(a.x) + (t0 + t) * a.xt + (int64_t)(h0 + h) * a.xh;
     elem* y = static_cast<elem*>(a.y) + (t0 + t) * a.yt + (int64_t)(h0 + h) * a.yh;
-    const bool turned = 16 * u < a.rot;
-    const int e0 = turned && !INTER ? 8 * u : 16 * u;
-    const int e1 = turned && !INTER ? 8 * u + half : 16 * u + 8;
-    float p[8], q[8];
-    load8<E>(x + e0, p);
-    load8<E>(x + e1, q);
+    const bool turned = 2 * P * u < a.rot;
+    const int e0 = turned && !INTER ? P * u : 2 * P * u;
+    const int e1 = turned && !INTER ? P * u + half : 2 * P * u + P;
+    float p[P], q[P];
+    load_step<E>(x + e0, p);
+    load_step<E>(x + e1, q);
     if (turned) {
-      const float2* c = cs + t * half + 8 * u;
+      const float2* c = cs + t * half + P * u;
       if (INTER) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 c0 = c[j], c1 = c[j + 4];
+        for (int j = 0; j < P / 2; ++j) {
+          const float2 c0 = c[j], c1 = c[j + P / 2];
           const float a0 = p[2 * j], b0 = p[2 * j + 1], a1 = q[2 * j], b1 = q[2 * j + 1];
           p[2 * j] = a0 * c0.x - b0 * c0.y;
           p[2 * j + 1] = b0 * c0.x + a0 * c0.y;
@@ -95,7 +113,7 @@ __global__ __launch_bounds__(256) void rope_vec(RopeArgs a, X axes) {
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < P; ++j) {
           const float2 v = c[j];
           const float b = q[j];
           q[j] = b * v.x + p[j] * v.y;
@@ -103,8 +121,8 @@ __global__ __launch_bounds__(256) void rope_vec(RopeArgs a, X axes) {
         }
       }
     }
-    store8<E>(y + e0, p);
-    store8<E>(y + e1, q);
+    store_step<E>(y + e0, p);
+    store_step<E>(y + e1, q);
   }
 }
 
@@ -173,9 +191,9 @@ hipError_t launch_any(bsq_dtype dt, Strided x, const int64_t* positions, const X
   // (2^23 workgroups of 256 threads: the most that one dimension of a grid takes)
   const bool vec = r.rot % 16 == 0 && D % 16 == 0 && wide(x, bytes) && wide(y, bytes) && T < (int64_t)1 << 23;
   if (vec) {
-    // about 512 steps of 16 elements to a workgroup where there are tokens enough, and otherwise
+    // about 512 steps to a workgroup where there are tokens enough, and otherwise
     // the heads spread so that a thread has one step
-    const int per_head = D / 16;
+    const int per_head = D / (dt == BSQ_FP32 ? 8 : 16);
     const int64_t steps = (int64_t)H * per_head;
     if (T * steps >= (int64_t)1024 * 512) {
       int64_t n = 512 / steps;
