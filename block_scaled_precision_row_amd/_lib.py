@@ -618,14 +618,17 @@ _DTYPES = {torch.bfloat16: BSQ_BF16, torch.float16: BSQ_FP16, torch.float32: BSQ
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from a build without a GPU
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # (tensors on a GPU: it is initialized)
 
 
 def _call(fn, device, *args):
     """lib.<fn>(*args, current stream) on `device`. (The handle alone: building a Stream object for it costs 2 us,
     as much as the launch.)"""
     index = device.index
-    if torch.cuda.current_device() == index:
-        _check(fn, getattr(lib, fn)(*args, _raw_stream(index)))
+    if _device_now() == index:
+        status = getattr(lib, fn)(*args, _raw_stream(index))
+        if status:
+            raise BsqError(fn, status)
         return
     with torch.cuda.device(device):
         _check(fn, getattr(lib, fn)(*args, _raw_stream(index)))
@@ -818,13 +821,13 @@ def bsq_rope_axes(x, positions, inv_freq, sections, order=BSQ_AXES_BLOCKS, layou
         yt, yh = (H * D if T > 1 else 0), (D if H > 1 else 0)
     else:
         yt, yh = _heads_like(y, shape, dtype, dev, "y")
-    axes = len(sections)
+    axes, pairs = len(sections), sum(sections)
     if positions.dtype is not torch.int64 or positions.shape != (T, axes) or positions.get_device() != dev.index:
         _like(positions, (T, axes), torch.int64, dev, "positions")
     pt, pa = positions.stride()
-    freq = _flat(inv_freq, (sum(sections),), torch.float32, dev, "inv_freq")
+    freq = _flat(inv_freq, (pairs,), torch.float32, dev, "inv_freq")
     _call("bsq_rope_axes", dev, _DTYPES[dtype], x.data_ptr(), xt, xh, positions.data_ptr(), pt, pa,
-          (ctypes.c_int64 * axes)(*sections), axes, order, freq, layout, attn_factor,
+          (_i64 * axes)(*sections), axes, order, freq, layout, attn_factor,
           BSQ_ROPE_BACKWARD if backward else 0, y.data_ptr(), yt, yh, T, H, D)
     return y
 
@@ -839,6 +842,15 @@ def _row_stride(x, shape, dtype, device, name):
     if sd != 1 and shape[1] > 1:
         raise ValueError("%s must have unit stride along its last dimension" % name)
     return x.data_ptr(), (st if shape[0] > 1 else 0)
+
+
+def _vector(x, n, dtype, device, name):
+    """Address of a dense vector of n elements."""
+    if x.dtype is not dtype or x.numel() != n or x.dim() != 1 or x.get_device() != device.index:
+        _like(x, (n,), dtype, device, name)
+    if not x.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return x.data_ptr()
 
 
 def _group_count(vectors, starts):
@@ -864,11 +876,11 @@ def _block(x, norm, eps, weight, bias, scale, shift, gate, post, post_weight, po
     w = b = pw = sc = sh = ga = None
     scs = shs = gas = 0
     if weight is not None:
-        w = _flat(weight, (dim,), dtype, dev, "weight")
+        w = _vector(weight, dim, dtype, dev, "weight")
     if bias is not None:
-        b = _flat(bias, (dim,), dtype, dev, "bias")
+        b = _vector(bias, dim, dtype, dev, "bias")
     if post_weight is not None:
-        pw = _flat(post_weight, (dim,), dtype, dev, "post_weight")
+        pw = _vector(post_weight, dim, dtype, dev, "post_weight")
     if scale is None and shift is None and gate is None:
         groups = 1 if starts is None else starts.shape[0] - 1
     else:
@@ -989,7 +1001,7 @@ def _epilogue(M, N, bias, act, gate, residual, starts, y, dev):
     bp = gp = rp = None
     gs = rs = 0
     if bias is not None:
-        bp = _flat(bias, (N,), bf16, dev, "bias")
+        bp = _vector(bias, N, bf16, dev, "bias")
     if gate is not None:
         groups = _group_count((gate,), starts)
         gp, gs = _row_stride(gate, (groups, N), bf16, dev, "gate")
@@ -1011,9 +1023,9 @@ def bsq_gemm_fp8r_q_epilogue(xq, x_scale, w, w_scale, bias=None, act=BSQ_ACT_NON
     None), all bf16 or None."""
     dev, (M, K), N = xq.device, xq.shape, w.shape[0]
     xp = _flat(xq, (M, K), torch.uint8, dev, "xq")
-    sp = _flat(x_scale, (M,), torch.float32, dev, "x_scale")
+    sp = _vector(x_scale, M, torch.float32, dev, "x_scale")
     wp = _flat(w, (N, K), torch.uint8, dev, "w")
-    wsp = _flat(w_scale, (N,), torch.float32, dev, "w_scale")
+    wsp = _vector(w_scale, N, torch.float32, dev, "w_scale")
     e, y, yp, ldy = _epilogue(M, N, bias, act, gate, residual, starts, y, dev)
     _call("bsq_gemm_fp8r_q_epilogue", dev, xp, sp, wp, wsp, e, yp, ldy, M, N, K)
     return y
@@ -1026,10 +1038,10 @@ def bsq_gemm_nvfp4_q_epilogue(xq, x_bscale, input_scale, w, w_bscale, w_scale2, 
     K = 2 * half
     xp = _flat(xq, (M, half), torch.uint8, dev, "xq")
     sp = _flat(x_bscale, (M, K // 16), torch.uint8, dev, "x_bscale")
-    ip = _flat(input_scale, (1,), torch.float32, dev, "input_scale")
+    ip = _vector(input_scale, 1, torch.float32, dev, "input_scale")
     wp = _flat(w, (N, half), torch.uint8, dev, "w")
     wsp = _flat(w_bscale, (N, K // 16), torch.uint8, dev, "w_bscale")
-    gp = _flat(w_scale2, (1,), torch.float32, dev, "w_scale2")
+    gp = _vector(w_scale2, 1, torch.float32, dev, "w_scale2")
     e, y, yp, ldy = _epilogue(M, N, bias, act, gate, residual, starts, y, dev)
     _call("bsq_gemm_nvfp4_q_epilogue", dev, xp, sp, ip, wp, wsp, gp, e, yp, ldy, M, N, K)
     return y

@@ -581,16 +581,18 @@ __device__ __forceinline__ float one(const void* p, int64_t at) {
   if constexpr (sizeof(typename E::elem) == 4) return static_cast<const float*>(p)[at];
   else return E::up(static_cast<const uint16_t*>(p)[at]);
 }
-// Columns are taken four at a time, by 8 x 8 lanes of a wave (quadruple, share) and 16 waves: 128 threads share the sum of
-// a column, so that a few hundred slots are a few loads each.
-constexpr int kCols = 8, kWaves = 16, kShares = 8 * kWaves;
+// Columns are taken four at a time, by 8 x 8 lanes of a wave (quadruple, share) and W waves: with 16 of them 128 threads
+// share the sum of a column, so that a few hundred slots are a few loads each; one wave where a group has few slots.
+constexpr int kCols = 8;
 
 __device__ __forceinline__ void add4(float4& a, float4 b) { a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 // sums[q] over the threads of a column: whole in the first 8 threads of the workgroup
+template <int W>
 struct ColumnSlots {
-  float4 s[3][kWaves][kCols];
+  float4 s[3][W][kCols];
 };
-__device__ __forceinline__ void column_sums(float4 (&v)[3], int need, ColumnSlots& slots) {
+template <int W>
+__device__ __forceinline__ void column_sums(float4 (&v)[3], int need, ColumnSlots<W>& slots) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
@@ -608,7 +610,7 @@ __device__ __forceinline__ void column_sums(float4 (&v)[3], int need, ColumnSlot
       if (!(need >> q & 1)) continue;
       v[q] = slots.s[q][0][threadIdx.x];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) add4(v[q], slots.s[q][w][threadIdx.x]);
+      for (int w = 1; w < W; ++w) add4(v[q], slots.s[q][w][threadIdx.x]);
     }
   }
   __syncthreads();  // (the slots are free again)
@@ -642,10 +644,10 @@ __device__ __forceinline__ void put_shared(const NormBackward& a, int col, const
 
 // The sums of each group: grid.x over columns, grid.y (striding) over groups. With one group also what all groups share;
 // otherwise, where that is asked for, the sums go to `group_sums` [groups][3][dim].
-template <class E>
-__global__ __launch_bounds__(64 * kWaves) void norm_group_sums(NormBackward a, int run, int need, const float* part_sums,
+template <class E, int W>
+__global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int run, int need, const float* part_sums,
                                                                 float* group_sums) {
-  __shared__ ColumnSlots slots;
+  __shared__ ColumnSlots<W> slots;
   const int share = threadIdx.x / kCols, col = 4 * (int)(blockIdx.x * kCols + threadIdx.x % kCols);
   const bool live = col < a.n.dim;
   const RowGroups& rg = a.n.groups;
@@ -665,7 +667,7 @@ __global__ __launch_bounds__(64 * kWaves) void norm_group_sums(NormBackward a, i
     if (r1 > r0 && live) {
       const int w1 = (r1 - 1) / run;
 #pragma unroll 4
-      for (int w = r0 / run + share; w <= w1; w += kShares) {
+      for (int w = r0 / run + share; w <= w1; w += 8 * W) {
         const float* p = part_sums + (int64_t)(w + g) * 3 * a.n.dim + col;
 #pragma unroll
         for (int q = 0; q < 3; ++q)
@@ -695,14 +697,14 @@ __global__ __launch_bounds__(64 * kWaves) void norm_group_sums(NormBackward a, i
   }
 }
 
-template <class E>
-__global__ __launch_bounds__(64 * kWaves) void norm_shared_sums(NormBackward a, const float* group_sums) {
-  __shared__ ColumnSlots slots;
+template <class E, int W>
+__global__ __launch_bounds__(64 * W) void norm_shared_sums(NormBackward a, const float* group_sums) {
+  __shared__ ColumnSlots<W> slots;
   const int share = threadIdx.x / kCols, col = 4 * (int)(blockIdx.x * kCols + threadIdx.x % kCols);
   const bool live = col < a.n.dim;
   float4 t[3] = {};
   if (live) {
-    for (int g = share; g < a.n.groups.groups; g += kShares) {
+    for (int g = share; g < a.n.groups.groups; g += 8 * W) {
       float4 s[3];
 #pragma unroll
       for (int q = 0; q < 3; ++q)
@@ -809,10 +811,13 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
   if ((a.dweight || a.dbias || a.dpost_weight) && groups > 1)
     sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + slot_bytes(a.n.rows, a.n.dim, groups));
   const unsigned cols = (unsigned)((a.n.dim + 4 * kCols - 1) / (4 * kCols));
-  hipLaunchKernelGGL(norm_group_sums<E>, dim3(cols, (unsigned)(groups < 65535 ? groups : 65535)), dim3(64 * kWaves),
-                     0, s, a, run, need, parts, sums);
+  const dim3 grid(cols, (unsigned)(groups < 65535 ? groups : 65535));
+  if (workers / groups < 16)
+    hipLaunchKernelGGL((norm_group_sums<E, 1>), grid, dim3(64), 0, s, a, run, need, parts, sums);
+  else
+    hipLaunchKernelGGL((norm_group_sums<E, 16>), grid, dim3(1024), 0, s, a, run, need, parts, sums);
   if ((e = hipGetLastError()) != hipSuccess || !sums) return e;
-  hipLaunchKernelGGL(norm_shared_sums<E>, dim3(cols), dim3(64 * kWaves), 0, s, a, sums);
+  hipLaunchKernelGGL((norm_shared_sums<E, 16>), dim3(cols), dim3(1024), 0, s, a, sums);
   return hipGetLastError();
 }
 

@@ -65,10 +65,10 @@ bsq::NormArgs norm_args(const bsq_block* b) {
 }
 bsq::Rows rows_of(const void* p, int64_t stride) { return bsq::Rows{const_cast<void*>(p), stride}; }
 
-// the workgroups of a launch (one row each at least) times their threads stay below 2^31
+// the threads of a launch (block_norm.hip has one workgroup a row, or four rows of up to 512) stay below 2^31
 bool launch_fits(int64_t rows, int64_t dim) {
-  const int64_t threads = dim <= 1024 ? 64 : dim <= 8192 ? 256 : 512;
-  return rows * threads < (int64_t)1 << 31;
+  const int64_t waves = dim <= 2048 ? (dim + 511) / 512 : (dim + 1023) / 1024;
+  return rows * waves * 64 < ((int64_t)1 << 31) - 256;
 }
 
 }  // namespace

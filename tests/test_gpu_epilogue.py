@@ -184,3 +184,20 @@ def test_captured_and_replayed(fmt):
             want = f(*args, **more)
             torch.cuda.synchronize()
             assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("fmt", ["fp8r", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(9, 200, 256), (200, 130, 512), (500, 1001, 256), (300, 8000, 256), (1030, 2049, 288),
+                                   (4096, 4096, 256)])
+def test_a_group_for_each_row(fmt, M, N, K):
+    """More groups in a tile than its gates are held for, their rows at odd places."""
+    f, _, args, v, mag = operands(fmt, M, N, K, M)
+    g = torch.Generator().manual_seed(N)
+    gate, residual = bf(g, M, N + 3)[:, 1:N + 1], bf(g, M, N)
+    check(f(*args, gate=gate, residual=residual), v, mag, K, None, "none", gate, residual, np.arange(M))
+    st = torch.arange(M + 1, dtype=torch.int32).cuda()
+    st[M // 2:] = M // 2                                          # and half of the rows without a group
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    f(*args, gate=gate, starts=st, y=y)
+    check(y, v, mag, K, None, "none", gate, None, np.where(np.arange(M) < M // 2, np.arange(M), -1))
+    assert torch.all(y[M // 2:] == 7.0)
