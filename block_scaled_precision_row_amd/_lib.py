@@ -972,24 +972,25 @@ def bsq_block_norm_backward(dy, dx_out, x_out, norm=BSQ_NORM_RMS, eps=1e-6, weig
     if dbranch is not None:
         hp, hs = _row_stride(dbranch, shape, dtype, dev, "dbranch")
     out = {"x": dx, "branch": dbranch if dbranch is not None or not of_branch else dx}
-    pointers = {}
-    for name, vector, size in (("scale", scale, (groups, D)), ("shift", shift, (groups, D)), ("gate", gate, (groups, D)),
-                               ("weight", weight, (D,)), ("bias", bias, (D,)), ("post_weight", post_weight, (D,))):
-        t = p = None
-        if vector is not None and (need is None or name in need):
-            t = torch.empty(size, dtype=torch.float32, device=dev)
-            p = t.data_ptr()
-        out[name], pointers[name] = t, p
+    # the vectors' gradients: those of the groups in one tensor, those that all share in another
+    vectors = []
+    for names, size in (((("scale", scale), ("shift", shift), ("gate", gate)), (groups, D)),
+                        ((("weight", weight), ("bias", bias), ("post_weight", post_weight)), (D,))):
+        asked = [name for name, v in names if v is not None and (need is None or name in need)]
+        grads = iter(torch.empty((len(asked), *size), dtype=torch.float32, device=dev).unbind(0) if asked else ())
+        for name, _ in names:
+            out[name] = t = next(grads) if name in asked else None
+            vectors.append(None if t is None else t.data_ptr())
     n = 0
     if workspace is None:
-        if T and any(pointers.values()):
+        if T and any(v is not None for v in vectors):
             n = lib.bsq_block_norm_workspace_bytes(T, D, groups)
             workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev:
         raise ValueError("workspace must be on %s" % dev)
     else:
         n = _nbytes(workspace)
-    _call("bsq_block_norm_backward", dev, block, yp, ys, dp, ds, op, os_, bp, bs, xp, xs, hp, hs, *pointers.values(),
+    _call("bsq_block_norm_backward", dev, block, yp, ys, dp, ds, op, os_, bp, bs, xp, xs, hp, hs, *vectors,
           None if workspace is None else workspace.data_ptr(), n)
     return out
 

@@ -642,40 +642,63 @@ __device__ __forceinline__ void put_shared(const NormBackward& a, int col, const
   if (a.dpost_weight) put4(a.dpost_weight, col, t[2]);
 }
 
-// The sums of each group: grid.x over columns, grid.y (striding) over groups. With one group also what all groups share;
-// otherwise, where that is asked for, the sums go to `group_sums` [groups][3][dim].
+// the workers of group g's rows: first to last (none: last < first)
+__device__ __forceinline__ void workers_of_group(const RowGroups& rg, int g, int run, int& first, int& last) {
+  int r0, r1;
+  if (rg.starts) {
+    const int limit = group_limit(rg);  // (the first group starts at 0, the last one ends there)
+    r0 = g == 0 ? 0 : rg.starts[g];
+    r1 = g == rg.groups - 1 ? limit : rg.starts[g + 1];
+    r0 = r0 < 0 ? 0 : r0;
+    r1 = r1 < limit ? r1 : limit;
+  } else {
+    r0 = g * rg.per;
+    r1 = r0 + rg.per;
+  }
+  first = r1 > r0 ? r0 / run : 0;
+  last = r1 > r0 ? (r1 - 1) / run : -1;
+}
+// this thread's share of group g's slots, four columns of each sum
+__device__ __forceinline__ void slot_share(const NormBackward& a, int g, int run, int need, const float* part_sums,
+                                           int col, int share, int shares, float4 (&s)[3]) {
+  int w, last;
+  workers_of_group(a.n.groups, g, run, w, last);
+#pragma unroll 4
+  for (w += share; w <= last; w += shares) {
+    const float* p = part_sums + (int64_t)(w + g) * 3 * a.n.dim + col;
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (need >> q & 1) add4(s[q], *reinterpret_cast<const float4*>(p + (int64_t)q * a.n.dim));
+  }
+}
+
+// The sums of the slots: grid.x over columns, grid.y (striding) over groups, starting with `from`, for the gradients that
+// each has of its own and, for `shared`, one more for those that all share. With `group_sums` [groups][3][dim] the groups' sums go there
+// instead, for norm_shared_sums.
 template <class E, int W>
-__global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int run, int need, const float* part_sums,
-                                                                float* group_sums) {
+__global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int run, int need, int from,
+                                                           int shared, const float* part_sums, float* group_sums) {
   __shared__ ColumnSlots<W> slots;
   const int share = threadIdx.x / kCols, col = 4 * (int)(blockIdx.x * kCols + threadIdx.x % kCols);
   const bool live = col < a.n.dim;
-  const RowGroups& rg = a.n.groups;
-  for (int g = blockIdx.y; g < rg.groups; g += gridDim.y) {
-    int r0, r1;
-    if (rg.starts) {
-      const int limit = group_limit(rg);  // (the first group starts at 0, the last one ends there)
-      r0 = g == 0 ? 0 : rg.starts[g];
-      r1 = g == rg.groups - 1 ? limit : rg.starts[g + 1];
-      r0 = r0 < 0 ? 0 : r0;
-      r1 = r1 < limit ? r1 : limit;
-    } else {
-      r0 = g * rg.per;
-      r1 = r0 + rg.per;
-    }
+  const int groups = a.n.groups.groups;
+  for (int g = from + blockIdx.y; g < groups + shared; g += gridDim.y) {
     float4 s[3] = {};
-    if (r1 > r0 && live) {
-      const int w1 = (r1 - 1) / run;
-#pragma unroll 4
-      for (int w = r0 / run + share; w <= w1; w += 8 * W) {
-        const float* p = part_sums + (int64_t)(w + g) * 3 * a.n.dim + col;
-#pragma unroll
-        for (int q = 0; q < 3; ++q)
-          if (need >> q & 1) add4(s[q], *reinterpret_cast<const float4*>(p + (int64_t)q * a.n.dim));
+    if (g == groups) {
+      for (int o = 0; o < groups && live; ++o) {
+        float4 t[3] = {};
+        slot_share(a, o, run, need, part_sums, col, share, 8 * W, t);
+        add_shared<E>(a, o, col, t, s);
       }
+    } else if (live) {
+      slot_share(a, g, run, need, part_sums, col, share, 8 * W, s);
     }
     column_sums(s, need, slots);
     if (!live || share != 0) continue;
+    if (g == groups) {
+      put_shared(a, col, s);
+      continue;
+    }
     const int64_t at = (int64_t)g * a.n.dim + col;
     if (a.dscale) {
       float4 d = s[0];
@@ -689,10 +712,6 @@ __global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int ru
     if (group_sums) {
 #pragma unroll
       for (int q = 0; q < 3; ++q) put4(group_sums, ((int64_t)g * 3 + q) * a.n.dim + col, s[q]);
-    } else if (rg.groups == 1) {
-      float4 t[3] = {};
-      add_shared<E>(a, g, col, s, t);
-      put_shared(a, col, t);
     }
   }
 }
@@ -727,6 +746,7 @@ constexpr int kForwardOne = 2048;
 // 20 waves 54 and 65 (workers of five waves do not share out evenly over four SIMDs); a worker of fewer rows writes
 // sums for fewer (1001 x 1536 fp32: 4 rows 24 us, 2 rows 31, 1 row 59).
 constexpr int kBackwardWaves = 12, kBackwardRows = 4;
+constexpr int kGroupsAlong = 64;  // up to here the sums that all groups share are taken along with the groups' own
 
 // ---- launches -----------------------------------------------------------------------
 
@@ -807,15 +827,18 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
     return go(std::false_type{}, chunks_t<4>{});
   });
   if (e != hipSuccess || !need) return e;
+  // what all groups share: along with the groups' own, or after them where there are many
+  const bool shared = a.dweight || a.dbias || a.dpost_weight, own = a.dscale || a.dshift || a.dgate;
   float* sums = nullptr;
-  if ((a.dweight || a.dbias || a.dpost_weight) && groups > 1)
+  if (shared && groups > kGroupsAlong)
     sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + slot_bytes(a.n.rows, a.n.dim, groups));
+  const int along = shared && !sums ? 1 : 0, from = own || sums ? 0 : groups, jobs = groups + along - from;
   const unsigned cols = (unsigned)((a.n.dim + 4 * kCols - 1) / (4 * kCols));
-  const dim3 grid(cols, (unsigned)(groups < 65535 ? groups : 65535));
-  if (workers / groups < 16)
-    hipLaunchKernelGGL((norm_group_sums<E, 1>), grid, dim3(64), 0, s, a, run, need, parts, sums);
+  const dim3 grid(cols, (unsigned)(jobs < 65535 ? jobs : 65535));
+  if (workers / groups < 16 && (!along || workers < 64))
+    hipLaunchKernelGGL((norm_group_sums<E, 1>), grid, dim3(64), 0, s, a, run, need, from, along, parts, sums);
   else
-    hipLaunchKernelGGL((norm_group_sums<E, 16>), grid, dim3(1024), 0, s, a, run, need, parts, sums);
+    hipLaunchKernelGGL((norm_group_sums<E, 16>), grid, dim3(1024), 0, s, a, run, need, from, along, parts, sums);
   if ((e = hipGetLastError()) != hipSuccess || !sums) return e;
   hipLaunchKernelGGL((norm_shared_sums<E, 16>), dim3(cols), dim3(1024), 0, s, a, sums);
   return hipGetLastError();
@@ -824,7 +847,7 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
 }  // namespace
 
 size_t block_norm_workspace(int64_t rows, int64_t dim, int64_t groups) {
-  return slot_bytes(rows, dim, groups) + (groups > 1 ? (size_t)groups * 3 * (size_t)dim * 4 : 0);
+  return slot_bytes(rows, dim, groups) + (groups > kGroupsAlong ? (size_t)groups * 3 * (size_t)dim * 4 : 0);
 }
 
 hipError_t launch_block_norm(bsq_dtype dt, const NormForward& a, hipStream_t s) {

@@ -368,3 +368,34 @@ def test_starts_without_vectors(D):
         assert np.all(np.abs(f64(got[k]) - ref[k]) <= tol[k] + 2.0 ** -23 * np.abs(ref[k])), k
     assert torch.all(pad[2, 41:] == 7.0)
     assert np.all(np.abs(f64(got["x"]) - ref["x"])[:41] <= (tol["x"] + rounded(ref["x"], torch.bfloat16))[:41])
+
+
+@pytest.mark.parametrize("T,groups", [(64, 64), (130, 65), (900, 3), (66000, 66000)])
+def test_sums_of_all_groups(T, groups):
+    """The gradients that all groups share, along with the groups' own and after them, and asked for alone."""
+    D = 64
+    v = vectors(T, T, D, "fp32", groups, **ALL)
+    group = np.arange(T) // (T // groups)
+    dy, do = torch.randn(2, T, D, generator=torch.Generator().manual_seed(T)).cuda()
+    x_out = v.pop("x")
+    dv = doubles(v)
+    args = dict(norm="layer", eps=EPS, post="rms", post_eps=POST_EPS)
+    if groups > 1000:   # (the oracle's sums by groups are a product with all of them: take those of the shared alone)
+        D_all = {k: t for k, t in dv.items()}
+        spread = {k: D_all[k][group] for k in ("scale", "shift", "gate")}
+        n = block.normed(f64(x_out), "layer", EPS)[0]
+        d = f64(dy) * (1 + spread["scale"])
+        got = L.bsq_block_norm_backward(dy, do, x_out, norm=L.BSQ_NORM_LAYER, eps=EPS, post=L.BSQ_NORM_RMS, post_eps=POST_EPS, **v)
+        chain = (T / 512 + groups / 128 + 64) * 2.0 ** -24 + 2.0 ** -16   # (2^-16: the errors of N, a term's at most)
+        assert np.all(np.abs(f64(got["weight"]) - (d * n).sum(0)) <= chain * np.abs(d * n).sum(0) + 2.0 ** -14 * np.abs(d).sum(0))
+        assert np.all(np.abs(f64(got["bias"]) - d.sum(0)) <= chain * np.abs(d).sum(0))
+        assert np.all(np.abs(f64(got["shift"]) - f64(dy)) == 0.0)
+        return
+    ref, tol = backward_bounds(f64(dy), f64(do), f64(x_out), group=group, groups=groups, **args, **dv)
+    call = lambda **kw: L.bsq_block_norm_backward(dy, do, x_out, norm=L.BSQ_NORM_LAYER, eps=EPS, post=L.BSQ_NORM_RMS,  # noqa: E731
+                                                  post_eps=POST_EPS, **v, **kw)
+    out = call()
+    for k in ("scale", "shift", "gate", "weight", "bias", "post_weight"):
+        assert np.all(np.abs(f64(out[k]) - ref[k]) <= tol[k] + 2.0 ** -23 * np.abs(ref[k])), k
+    alone = call(need=("weight", "bias", "post_weight"))
+    assert all(torch.equal(alone[k], out[k]) for k in ("weight", "bias", "post_weight")) and alone["x"] is None
