@@ -21,7 +21,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quant.hip", "dequant.hip", "gemm_fp8.hip", "gemm_dec.hip", "gemm_w4a4.hip", "gemm_skinny.hip", "gemm_a16.hip", "lora.hip", "scratch.hip", "bsq_api.cpp",
            "rope.hip", "kv_append.hip", "kv_attn.hip", "kv_prompt.hip", "gemm_int4.hip", "bsq_serve.cpp",
-           "block_norm.hip", "gemm_fp8_epilogue.hip", "gemm_w4a4_epilogue.hip", "bsq_block.cpp"]
+           "block_norm.hip", "gemm_fp8_epilogue.hip", "gemm_w4a4_epilogue.hip",
+           "gemm_w4a4_any_epilogue.hip", "bsq_block.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",

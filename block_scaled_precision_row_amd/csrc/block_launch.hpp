@@ -67,10 +67,10 @@ struct Epilogue {
   RowGroups groups;
   int act;  // bsq_act
 };
-// the few-token kernels (W8A8, W4A4), the tiled W8A8 ones, the tiled W4A4 ones (K % 256 == 0, and any K)
+// the few-token kernels (W8A8, W4A4), the tiled W8A8 ones, the tiled W4A4 ones (K % 256 == 0, and any other K)
 hipError_t launch_gemm_skinny_epilogue(DecMode mode, const DecArgs& a, const Epilogue& ep, hipStream_t s);
 hipError_t launch_gemm_fp8_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s);
 hipError_t launch_gemm_w4a4_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s);
-hipError_t launch_gemm_dec_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s);
+hipError_t launch_gemm_w4a4_any_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s);
 
 }  // namespace bsq

@@ -423,7 +423,7 @@ bsq_status bsq_gemm_nvfp4_q_epilogue(const uint8_t* xq, const uint8_t* x_bscale,
   hipError_t r;
   if (route_skinny(bsq::kW4A4, a)) r = bsq::launch_gemm_skinny_epilogue(bsq::kW4A4, a, e, stream);
   else if (bsq::gemm_w4a4_supported(a)) r = bsq::launch_gemm_w4a4_epilogue(a, e, stream);
-  else r = bsq::launch_gemm_dec_epilogue(a, e, stream);
+  else r = bsq::launch_gemm_w4a4_any_epilogue(a, e, stream);
   return r == hipSuccess ? BSQ_OK : hip_fail(r);
 }
 

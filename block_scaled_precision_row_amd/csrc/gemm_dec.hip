@@ -27,7 +27,6 @@
 // of E2M1 plus 4 block scales, 64 bytes of E4M3 or 128 bytes of bf16),
 // decodes it in registers and writes 8 swizzled 16-byte chunks.
 #include "bsq_launch.hpp"
-#include "epilogue.hpp"
 #include "gemm_common.hpp"
 
 namespace bsq {
@@ -164,9 +163,9 @@ struct ModeTraits<kW8A16> {
   static constexpr bool F16 = false;
 };
 
-// Finish: what becomes of the scaled sums (W4A4; TileEpilogue of epilogue.hpp); NoFinish: y is their bf16
-template <int MODE, int BM, int BN, bool LORA, class Finish>
-__device__ __forceinline__ void dec_tile(const DecArgs& a, const Finish& finish) {
+template <int MODE, int BM, int BN, bool LORA>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_dec_kernel(DecArgs a) {
   using T = ModeTraits<MODE>;
   constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
   constexpr int ROWS = BM + BN, STAGE = ROWS * 128;
@@ -283,19 +282,6 @@ __device__ __forceinline__ void dec_tile(const DecArgs& a, const Finish& finish)
   const bool vec_ok = (a.ldy & 3) == 0;  // 8-byte stores need 4-element aligned rows
   float alpha = 1.0f;
   if (MODE == kW4A4) alpha = a.gx[0] * a.gw[0];
-  if constexpr (!std::is_same<Finish, gemm::NoFinish>::value) {  // (every wave has passed the last stage's barrier)
-    constexpr int TROW = BN * 2 + 16;
-    static_assert(MODE == kW4A4 && !LORA && BM * TROW <= 2 * STAGE, "the output tile fits the stage buffers");
-    auto scaled = [&](int i, int j, int g, const float4* bias) {
-      const v16f& A = acc[i][j];
-      if (!bias) return make_float4(A[4 * g] * alpha, A[4 * g + 1] * alpha, A[4 * g + 2] * alpha, A[4 * g + 3] * alpha);
-      const float4 b = *bias;
-      return make_float4(fmaf(A[4 * g], alpha, b.x), fmaf(A[4 * g + 1], alpha, b.y), fmaf(A[4 * g + 2], alpha, b.z),
-                         fmaf(A[4 * g + 3], alpha, b.w));
-    };
-    finish.template tile<BM, BN, TROW, TN, TM>(smem, a.y, a.ldy, M, N, m0, n0, wm * WM, wn * WN, tid, false, scaled);
-    return;
-  }
   if (MODE == kW4A16) alpha = a.gw[0];
   if constexpr (LORA) {
     // with an adapter: y = bf16(acc * scale + T B^T), the adapter's MFMAs accumulating onto the
@@ -348,18 +334,6 @@ __device__ __forceinline__ void dec_tile(const DecArgs& a, const Finish& finish)
 }
 
 template <int MODE, int BM, int BN, bool LORA>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void gemm_dec_kernel(DecArgs a) {
-  dec_tile<MODE, BM, BN, LORA>(a, gemm::NoFinish{});
-}
-// W4A4 with an epilogue on the sums
-template <int BM, int BN, int ACT>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void gemm_dec_epilogue_kernel(DecArgs a, gemm::TileEpilogue<ACT> e) {
-  dec_tile<kW4A4, BM, BN, false>(a, e);
-}
-
-template <int MODE, int BM, int BN, bool LORA>
 hipError_t run_kernel(const DecArgs& a, hipStream_t s) {
   const size_t lds = 2 * (size_t)(BM + BN) * 128;
   static std::atomic<unsigned long long> lds_set{0};
@@ -384,27 +358,7 @@ hipError_t pick(const DecArgs& a, hipStream_t s) {
   return run<MODE, 128, 128>(a, s);
 }
 
-template <int BM, int BN>
-hipError_t run_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s) {
-  const int tiles = (int)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN));
-  return gemm::with_kind<gemm::TileEpilogue>(ep, [&](auto e) {
-    constexpr int ACT = decltype(e)::act;
-    const size_t lds = 2 * (size_t)(BM + BN) * 128;
-    static std::atomic<unsigned long long> lds_set{0};
-    hipError_t err =
-        ensure_lds_limit(reinterpret_cast<const void*>(&gemm_dec_epilogue_kernel<BM, BN, ACT>), (int)lds, lds_set);
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((gemm_dec_epilogue_kernel<BM, BN, ACT>), dim3(tiles), dim3(kThreads), lds, s, a, e);
-    return hipGetLastError();
-  });
-}
-
 }  // namespace
-
-// W4A4 with K % 256 != 0, with an epilogue: 128 x 128 tiles, as such linears take below 192 of the larger ones
-hipError_t launch_gemm_dec_epilogue(const DecArgs& a, const Epilogue& ep, hipStream_t s) {
-  return run_epilogue<128, 128>(a, ep, s);
-}
 
 hipError_t launch_gemm_dec(DecMode mode, const DecArgs& a, hipStream_t s) {
   switch (mode) {

@@ -242,9 +242,23 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
       dma16(isA ? rw : rx, lb, voff[i], load_addr(i, kt * kStageK).soff);
     };
     auto abuf = [&](int kt) { return smem + (kt % NS) * C::STAGE; };
-    const int nk = K / kStageK;
+    // With an epilogue K may be any: the chunks past K of a partial last stage are marked out of range
+    constexpr bool kAnyK = kFinish;
+    auto dma_last = [&](int i, int kt) {
+      const bool isA = i < LA;
+      const int ld = wave + 4 * (isA ? i : i - LA);
+      const uint32_t lb = lds0 + (uint32_t)((kt % NS) * C::STAGE) + (isA ? 0u : (uint32_t)C::A_BYTES) + ld * 1024;
+      const DmaAddr at = load_addr(i, kt * kStageK);
+      dma16(isA ? rw : rx, lb, at.voff, at.soff);
+    };
+    const int nk = kAnyK ? (K + kStageK - 1) / kStageK : K / kStageK;
+    if (kAnyK && nk == 1) {
 #pragma unroll
-    for (int i = 0; i < LD; ++i) dma(i, 0);
+      for (int i = 0; i < LD; ++i) dma_last(i, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) dma(i, 0);
+    }
     // kLoraLate(2): rank values 0..63 go to the stage buffer of stage nk - 2 once it is read
     // (stage buffer 1 for a single stage), values 64..127 to that of stage nk - 1
     static_assert(LL < kLoraLate || C::STAGE == (BM + BN) * 128, "64 rank values of the rows fill one stage buffer");
@@ -253,8 +267,13 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
         lora_stage<BM, BN, 128>(lt, lb, M, N, m0, n0, rank, k_lo, lds0 + (uint32_t)(buf * C::STAGE), wave, lane);
     };
     if (nk > 1) {
+      if (kAnyK && nk == 2) {
 #pragma unroll
-      for (int i = 0; i < LD; ++i) dma(i, 1);
+        for (int i = 0; i < LD; ++i) dma_last(i, 1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) dma(i, 1);
+      }
       wait_vmcnt<LD>();
     } else {
       lora_late(1, 0);
@@ -266,8 +285,8 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
 #pragma unroll
     for (int j = 0; j < TM; ++j) b0[j] = frag(abuf(0) + C::A_BYTES, rowb + 32 * j, lh, 0);
 
-    auto iter = [&](int s, auto fetch, auto last) {
-      constexpr bool F = decltype(fetch)::value, LAST = decltype(last)::value;
+    auto iter = [&](int s, auto fetch, auto last, auto tail) {
+      constexpr bool F = decltype(fetch)::value, LAST = decltype(last)::value, TAIL = decltype(tail)::value;
       const uint8_t* ca = abuf(s);
       const uint8_t* cb = ca + C::A_BYTES;
 #pragma unroll
@@ -308,7 +327,11 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
         const int i = k / TM, j = k % TM;
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a1[i], b1[j], acc[i][j], 0, 0, 0, 0, 0, 0);
         if constexpr (F) {
-          if (k < LD) dma(k, s + 2);
+          if constexpr (TAIL) {
+            if (k < LD) dma_last(k, s + 2);
+          } else {
+            if (k < LD) dma(k, s + 2);
+          }
         }
         if (k >= KD) {
 #pragma unroll
@@ -322,7 +345,10 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
       }
       if constexpr (F) {
 #pragma unroll
-        for (int di = NM; di < LD; ++di) dma(di, s + 2);
+        for (int di = NM; di < LD; ++di) {
+          if constexpr (TAIL) dma_last(di, s + 2);
+          else dma(di, s + 2);
+        }
       }
       constexpr int done = (NM - KD) * RPM;
 #pragma unroll
@@ -331,10 +357,15 @@ __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const f
         else a0[f - TM] = frag(na, rowa + 32 * (f - TM), lh, 0);
       }
     };
+    using Yes = std::true_type;
+    using No = std::false_type;
     int s = 0;
-    for (; s + 2 < nk; ++s) iter(s, std::true_type{}, std::false_type{});
-    for (; s + 1 < nk; ++s) iter(s, std::false_type{}, std::false_type{});
-    iter(s, std::false_type{}, std::integral_constant<bool, !LORA && !kFinish>{});
+    for (; s + (kAnyK ? 3 : 2) < nk; ++s) iter(s, Yes{}, No{}, No{});
+    if constexpr (kAnyK) {
+      for (; s + 2 < nk; ++s) iter(s, Yes{}, No{}, Yes{});  // the last stage's loads
+    }
+    for (; s + 1 < nk; ++s) iter(s, No{}, No{}, No{});
+    iter(s, No{}, std::integral_constant<bool, !LORA && !kFinish>{}, No{});
   } else {
   // prologue: NS stages in flight, wait for the first
 #pragma unroll

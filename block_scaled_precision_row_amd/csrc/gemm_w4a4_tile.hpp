@@ -66,9 +66,51 @@ __device__ __forceinline__ uint32_t dword_of(const uint4& q) {
   return T == 0 ? q.x : T == 1 ? q.y : T == 2 ? q.z : q.w;
 }
 
-// Finish: what becomes of the scaled sums (TileEpilogue of epilogue.hpp); NoFinish: y is their bf16.
+// The block scales of a stage, for any K (K % 256 != 0: rows of scales are then not 16-byte aligned, which an LDS DMA
+// asks for): 16 bytes of each W and Xq row into registers, at any address, and from there to where the DMA would have put
+// them. Scales past K and rows past the matrix are 0 (the codes there are read as 0; a scale's NaN must not meet them).
+template <int BM, int BN>
+struct ScaleRows {
+  static constexpr int N = (BM + BN + kThreads - 1) / kThreads;
+  struct __attribute__((packed, aligned(2))) Any {
+    uint32_t w[4];
+  };
+  uint4 v[N];
+  __device__ __forceinline__ void load(const DecArgs& a, int m0, int n0, int kt, int tid) {
+    const int M = (int)a.M, K = (int)a.K, ks = K >> 4, at = kt * (kStageK / 16), left = ks - at;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int r = tid + j * kThreads;
+      const bool w = r < BN;
+      const int row = w ? n0 + r : m0 + r - BN;
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (left <= 0 || r >= BM + BN || row >= (w ? (int)a.N : M)) continue;
+      const uint8_t* p = (w ? a.ws : a.xs) + (int64_t)row * ks + at;
+      if (left >= 16) {
+        const Any x = *reinterpret_cast<const Any*>(p);
+        v[j] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+      } else {  // (an even number of them: K % 32 == 0)
+        uint32_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (2 * e < left) x[e >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+        v[j] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* stage, int tid) const {
+    using C = W4Cfg<BM, BN>;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int r = tid + j * kThreads;
+      if (r < BM + BN) *reinterpret_cast<uint4*>(stage + (r < BN ? C::SA_OFF + 16 * r : C::SB_OFF + 16 * (r - BN))) = v[j];
+    }
+  }
+};
+
+// Finish: what becomes of the scaled sums (TileEpilogue of epilogue.hpp); NoFinish: y is their bf16. ANYK: K % 256 != 0.
 // One output tile: workgroup `bid` of the grid of BM x BN tiles over M x N.
-template <int BM, int BN, bool LORA, class Finish = NoFinish>
+template <int BM, int BN, bool LORA, class Finish = NoFinish, bool ANYK = false>
 __device__ __forceinline__ void w4a4_tile(const DecArgs& a, int bid, const Finish& finish = Finish{}) {
   constexpr bool kFinish = !std::is_same<Finish, NoFinish>::value;
   using C = W4Cfg<BM, BN>;
@@ -98,13 +140,18 @@ __device__ __forceinline__ void w4a4_tile(const DecArgs& a, int bid, const Finis
   }
 
   // fetch stage kt into buffer kt % 2 (stages past K read as zeros)
+  ScaleRows<BM, BN> scale_rows;  // (ANYK)
   auto issue_stage = [&](int kt) {
     const int kb = kt * kStageK;
     const uint32_t base = lds0 + (uint32_t)((kt & 1) * C::STAGE);
     dma_region<typename C::RA>(rwq, base + C::A_OFF, wave, lane, kp, kb >> 1, kb, K);
     dma_region<typename C::RB>(rxq, base + C::B_OFF, wave, lane, kp, kb >> 1, kb, K);
-    dma_region<typename C::SA>(rws, base + C::SA_OFF, wave, lane, ks, kb >> 4, kb, K);
-    dma_region<typename C::SB>(rxs, base + C::SB_OFF, wave, lane, ks, kb >> 4, kb, K);
+    if constexpr (ANYK) {
+      scale_rows.load(a, m0, n0, kt, tid);
+    } else {
+      dma_region<typename C::SA>(rws, base + C::SA_OFF, wave, lane, ks, kb >> 4, kb, K);
+      dma_region<typename C::SB>(rxs, base + C::SB_OFF, wave, lane, ks, kb >> 4, kb, K);
+    }
   };
 
   v16f acc[TN][TM];
@@ -115,7 +162,7 @@ __device__ __forceinline__ void w4a4_tile(const DecArgs& a, int bid, const Finis
 
   const int lr = lane & 31, lh = lane >> 5;
   const int rowa = wn * C::WN + lr, rowb = wm * C::WM + lr;  // region-local rows
-  const int nk = K / kStageK;
+  const int nk = ANYK ? (K + kStageK - 1) / kStageK : K / kStageK;
 
   Raw r0a[TN], r0b[TM], r1a[TN], r1b[TM];  // packed operands of the current / next K group
   uint2 s0a[TN], s0b[TM], s1a[TN], s1b[TM];  // block scales of the current / next stage
@@ -244,6 +291,7 @@ __device__ __forceinline__ void w4a4_tile(const DecArgs& a, int bid, const Finis
     issue_stage(0);
     wait_vmcnt<0>();
   }
+  if constexpr (ANYK) scale_rows.store(smem, tid);
   __syncthreads();
   issue_stage(1);
   read_raw<TN, TM>(smem, C::A_OFF, C::B_OFF, rowa, rowb, lh, 0, r0a, r0b);
@@ -266,6 +314,7 @@ __device__ __forceinline__ void w4a4_tile(const DecArgs& a, int bid, const Finis
     group(r1a, r1b, r0a, r0b, cur, 2, csa, csb, F{});
     group(r0a, r0b, r1a, r1b, cur, 3, csa, csb, F{});
     wait_vmcnt<0>();
+    if constexpr (ANYK) scale_rows.store(smem + ((s + 1) & 1) * C::STAGE, tid);
     __syncthreads();
     if (s + 2 < nk) issue_stage(s + 2);
     if constexpr (!LAST) read_scales<TN, TM>(nxt, C::SA_OFF, C::SB_OFF, rowa, rowb, lh, nsa, nsb);
