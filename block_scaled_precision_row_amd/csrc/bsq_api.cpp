@@ -391,6 +391,13 @@ bsq_status check_epilogue(const bsq_epilogue* p, const uint16_t* y, int64_t ldy,
   }
   return BSQ_OK;
 }
+// Few tokens: as the plain linears, but past 64 rows only while the few-token kernels' workgroups (32 columns x 64 rows)
+// fit one round on the compute units; a second round costs more than the tiles' deeper K loops (cold operands, 96 rows,
+// N x K, few-token kernels against tiles: nvfp4 4096 x 4096 15.8 / 17.6 us, 5504 x 4096 26.8 / 18.3, 5504 x 6752
+// 42.8 / 31.4; fp8r 4096 x 4096 12.9 / 13.2, 5504 x 4096 20.0 / 13.8, 5504 x 6752 28.5 / 24.5).
+bool route_skinny_epilogue(bsq::DecMode mode, const bsq::DecArgs& a) {
+  return route_skinny(mode, a) && (a.M <= 64 || ((a.N + 31) / 32) * ((a.M + 63) / 64) <= 256);
+}
 }  // namespace
 
 bsq_status bsq_gemm_fp8r_q_epilogue(const uint8_t* xq, const float* x_scale, const uint8_t* w, const float* w_scale,
@@ -403,8 +410,8 @@ bsq_status bsq_gemm_fp8r_q_epilogue(const uint8_t* xq, const float* x_scale, con
   if ((st = check_device()) != BSQ_OK) return st;
   bsq::DecArgs a{};
   a.xq = xq; a.sx = x_scale; a.w = w; a.sw = w_scale; a.y = y; a.ldy = ldy; a.M = M; a.N = N; a.K = K;
-  const hipError_t r = route_skinny(bsq::kW8A8, a) ? bsq::launch_gemm_skinny_epilogue(bsq::kW8A8, a, e, stream)
-                                                   : bsq::launch_gemm_fp8_epilogue(a, e, stream);
+  const hipError_t r = route_skinny_epilogue(bsq::kW8A8, a) ? bsq::launch_gemm_skinny_epilogue(bsq::kW8A8, a, e, stream)
+                                                            : bsq::launch_gemm_fp8_epilogue(a, e, stream);
   return r == hipSuccess ? BSQ_OK : hip_fail(r);
 }
 
@@ -421,7 +428,7 @@ bsq_status bsq_gemm_nvfp4_q_epilogue(const uint8_t* xq, const uint8_t* x_bscale,
   a.xq = xq; a.xs = x_bscale; a.gx = input_scale; a.w = w; a.ws = w_bscale; a.gw = w_scale2;
   a.y = y; a.ldy = ldy; a.M = M; a.N = N; a.K = K;
   hipError_t r;
-  if (route_skinny(bsq::kW4A4, a)) r = bsq::launch_gemm_skinny_epilogue(bsq::kW4A4, a, e, stream);
+  if (route_skinny_epilogue(bsq::kW4A4, a)) r = bsq::launch_gemm_skinny_epilogue(bsq::kW4A4, a, e, stream);
   else if (bsq::gemm_w4a4_supported(a)) r = bsq::launch_gemm_w4a4_epilogue(a, e, stream);
   else r = bsq::launch_gemm_w4a4_any_epilogue(a, e, stream);
   return r == hipSuccess ? BSQ_OK : hip_fail(r);

@@ -235,3 +235,12 @@ def test_a_nan_scale_stays_in_its_row(M, N, K):
     nan[33], nan[:, 64] = True, True
     assert torch.equal(torch.isnan(y), nan)
     assert torch.equal(y[~nan], clean[~nan])
+
+
+@pytest.mark.parametrize("fmt", ["fp8r", "nvfp4"])
+@pytest.mark.parametrize("M,N", [(64, 5504), (65, 4096), (65, 4097), (128, 4100), (128, 7999)])
+def test_few_rows_and_many_columns(fmt, M, N):
+    f, _, args, v, bound = operands(fmt, M, N, 544, M + N)
+    g = torch.Generator().manual_seed(M)
+    bias, residual, gate = bf(g, N), bf(g, M, N), bf(g, 1, N)
+    check(f(*args, bias=bias, act=ACTS["gelu"], residual=residual, gate=gate), v, bound, bias, "gelu", gate, residual, None)
