@@ -642,8 +642,8 @@ __device__ __forceinline__ void put_shared(const NormBackward& a, int col, const
   if (a.dpost_weight) put4(a.dpost_weight, col, t[2]);
 }
 
-// the workers of group g's rows: first to last (none: last < first)
-__device__ __forceinline__ void workers_of_group(const RowGroups& rg, int g, int run, int& first, int& last) {
+// the workers of group g's rows: first to last (none: last < first); whether it has rows
+__device__ __forceinline__ bool workers_of_group(const RowGroups& rg, int g, int run, int& first, int& last) {
   int r0, r1;
   if (rg.starts) {
     const int limit = group_limit(rg);  // (the first group starts at 0, the last one ends there)
@@ -657,12 +657,14 @@ __device__ __forceinline__ void workers_of_group(const RowGroups& rg, int g, int
   }
   first = r1 > r0 ? r0 / run : 0;
   last = r1 > r0 ? (r1 - 1) / run : -1;
+  return r1 > r0;
 }
-// this thread's share of group g's slots, four columns of each sum
-__device__ __forceinline__ void slot_share(const NormBackward& a, int g, int run, int need, const float* part_sums,
+// this thread's share of group g's slots, four columns of each sum; whether the group has rows (the vectors of one
+// without may hold anything, NaN too, and do not count)
+__device__ __forceinline__ bool slot_share(const NormBackward& a, int g, int run, int need, const float* part_sums,
                                            int col, int share, int shares, float4 (&s)[3]) {
   int w, last;
-  workers_of_group(a.n.groups, g, run, w, last);
+  const bool any = workers_of_group(a.n.groups, g, run, w, last);
 #pragma unroll 4
   for (w += share; w <= last; w += shares) {
     const float* p = part_sums + (int64_t)(w + g) * 3 * a.n.dim + col;
@@ -670,11 +672,12 @@ __device__ __forceinline__ void slot_share(const NormBackward& a, int g, int run
     for (int q = 0; q < 3; ++q)
       if (need >> q & 1) add4(s[q], *reinterpret_cast<const float4*>(p + (int64_t)q * a.n.dim));
   }
+  return any;
 }
 
 // The sums of the slots: grid.x over columns, grid.y (striding) over groups, starting with `from`, for the gradients that
-// each has of its own and, for `shared`, one more for those that all share. With `group_sums` [groups][3][dim] the groups' sums go there
-// instead, for norm_shared_sums.
+// each has of its own and, for `shared`, one more for those that all share. With `group_sums` [groups][3][dim] the groups'
+// sums go there too, for norm_shared_sums.
 template <class E, int W>
 __global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int run, int need, int from,
                                                            int shared, const float* part_sums, float* group_sums) {
@@ -684,14 +687,14 @@ __global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int ru
   const int groups = a.n.groups.groups;
   for (int g = from + blockIdx.y; g < groups + shared; g += gridDim.y) {
     float4 s[3] = {};
+    bool any = false;
     if (g == groups) {
       for (int o = 0; o < groups && live; ++o) {
         float4 t[3] = {};
-        slot_share(a, o, run, need, part_sums, col, share, 8 * W, t);
-        add_shared<E>(a, o, col, t, s);
+        if (slot_share(a, o, run, need, part_sums, col, share, 8 * W, t)) add_shared<E>(a, o, col, t, s);
       }
     } else if (live) {
-      slot_share(a, g, run, need, part_sums, col, share, 8 * W, s);
+      any = slot_share(a, g, run, need, part_sums, col, share, 8 * W, s);
     }
     column_sums(s, need, slots);
     if (!live || share != 0) continue;
@@ -703,12 +706,14 @@ __global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int ru
     if (a.dscale) {
       float4 d = s[0];
       const float4 zero = make_float4(0, 0, 0, 0);
-      if (a.n.weight) d = fma4(d, four<E>(a.n.weight, col), zero);
-      if (a.n.bias) d = fma4(four<E>(a.n.bias, col), s[1], d);
+      if (any && a.n.weight) d = fma4(d, four<E>(a.n.weight, col), zero);
+      if (any && a.n.bias) d = fma4(four<E>(a.n.bias, col), s[1], d);
       put4(a.dscale, at, d);
     }
     if (a.dshift) put4(a.dshift, at, s[1]);
-    if (a.dgate) put4(a.dgate, at, a.n.post_weight ? fma4(s[2], four<E>(a.n.post_weight, col), make_float4(0, 0, 0, 0)) : s[2]);
+    if (a.dgate)
+      put4(a.dgate, at,
+           any && a.n.post_weight ? fma4(s[2], four<E>(a.n.post_weight, col), make_float4(0, 0, 0, 0)) : s[2]);
     if (group_sums) {
 #pragma unroll
       for (int q = 0; q < 3; ++q) put4(group_sums, ((int64_t)g * 3 + q) * a.n.dim + col, s[q]);
@@ -717,13 +722,15 @@ __global__ __launch_bounds__(64 * W) void norm_group_sums(NormBackward a, int ru
 }
 
 template <class E, int W>
-__global__ __launch_bounds__(64 * W) void norm_shared_sums(NormBackward a, const float* group_sums) {
+__global__ __launch_bounds__(64 * W) void norm_shared_sums(NormBackward a, int run, const float* group_sums) {
   __shared__ ColumnSlots<W> slots;
   const int share = threadIdx.x / kCols, col = 4 * (int)(blockIdx.x * kCols + threadIdx.x % kCols);
   const bool live = col < a.n.dim;
   float4 t[3] = {};
   if (live) {
     for (int g = share; g < a.n.groups.groups; g += 8 * W) {
+      int w, last;
+      if (!workers_of_group(a.n.groups, g, run, w, last)) continue;
       float4 s[3];
 #pragma unroll
       for (int q = 0; q < 3; ++q)
@@ -840,7 +847,7 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
   else
     hipLaunchKernelGGL((norm_group_sums<E, 16>), grid, dim3(1024), 0, s, a, run, need, from, along, parts, sums);
   if ((e = hipGetLastError()) != hipSuccess || !sums) return e;
-  hipLaunchKernelGGL((norm_shared_sums<E, 16>), dim3(cols), dim3(1024), 0, s, a, sums);
+  hipLaunchKernelGGL((norm_shared_sums<E, 16>), dim3(cols), dim3(1024), 0, s, a, run, sums);
   return hipGetLastError();
 }
 

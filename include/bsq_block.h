@@ -15,8 +15,9 @@
  *   group_starts  int32 [groups + 1] device, 4-byte aligned: group g has rows
  *     group_starts[g] to group_starts[g + 1] - 1 (none, if they are equal). It
  *     starts at 0 and does not decrease. Rows from group_starts[groups] on belong to
- *     no group: not written, and without effect. Where it decreases or leaves [0, rows], which vectors a row
- *     takes, and what is written for it, is not defined; nothing outside the call's tensors is read or written.
+ *     no group: not written, and without effect, as the vectors of a group without rows.
+ *     Where it decreases or leaves [0, rows], which vectors a row takes, and what is
+ *     written for it, is not defined; nothing outside the call's tensors is read or written.
  *   group_starts NULL: each group has rows / groups consecutive rows
  *     (rows % groups == 0, BSQ_ERR_SHAPE otherwise).
  * 1 <= groups <= 2^24 (1 where a call has no such vectors).

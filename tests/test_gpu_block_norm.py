@@ -399,3 +399,27 @@ def test_sums_of_all_groups(T, groups):
         assert np.all(np.abs(f64(out[k]) - ref[k]) <= tol[k] + 2.0 ** -23 * np.abs(ref[k])), k
     alone = call(need=("weight", "bias", "post_weight"))
     assert all(torch.equal(alone[k], out[k]) for k in ("weight", "bias", "post_weight")) and alone["x"] is None
+
+
+@pytest.mark.parametrize("T,groups", [(40, 5), (300, 70)])
+def test_vectors_of_groups_without_rows_do_not_count(T, groups):
+    """They may hold anything: the same gradients as with ones there, and zeros for the groups themselves, whatever the
+    vectors that all share hold."""
+    D = 776
+    v = vectors(11, T, D, "fp32", groups, branch=1, gate=1, scale=1, shift=1, weight=1, bias=1, post_weight=1)
+    n = [T // 2 if g in (1, 3) else 0 for g in range(groups)]
+    st = torch.tensor([0, *np.cumsum(n)], dtype=torch.int32).cuda()
+    without = torch.tensor([k == 0 for k in n], device="cuda")
+    dy, x = torch.randn(T, D, device="cuda"), v.pop("x")
+    outs = []
+    for fill in (1.0, float("nan")):
+        for k in ("gate", "scale", "shift"):
+            v[k][without] = fill
+        outs.append(L.bsq_block_norm_backward(dy, x, x, norm=L.BSQ_NORM_LAYER, post=L.BSQ_NORM_RMS, starts=st, **v))
+    for k, t in outs[0].items():
+        assert torch.isfinite(t).all() and torch.equal(t, outs[1][k]), k
+    for k in ("weight", "bias", "post_weight"):
+        v[k][5] = float("inf")
+    out = L.bsq_block_norm_backward(dy, x, x, norm=L.BSQ_NORM_LAYER, post=L.BSQ_NORM_RMS, starts=st, **v)
+    for k in ("gate", "scale", "shift"):
+        assert torch.all(out[k][without] == 0), k
