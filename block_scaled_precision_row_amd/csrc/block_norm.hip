@@ -1,8 +1,9 @@
 // The gated residual with the norms before and after it, and its gradient (include/bsq_block.h).
 //
-// Bound by memory: a row is read once, held in fp32 registers by the waves of one worker, and written once; a worker
-// takes several rows, with the next one's loads under way while it computes one, and keeps the vectors of its group in
-// registers. A sum over the row is one DPP reduction in each wave and, where a worker has several, one exchange through
+// Bound by memory: a row is read once, held in registers by the waves of one worker, and written once. Forward, a worker
+// has one row, and other workers' loads run under its sums (several rows with the next one's loads under way: 111 us
+// where this takes 64); backward it takes several, with the next one's loads under way, and keeps the vectors and the
+// columns' sums in registers. A sum over the row is one DPP reduction in each wave and, where a worker has several, one exchange through
 // LDS; the variance is taken about the mean (a second reduction) rather than from the squares, which would cancel for
 // rows far from zero.
 #include <type_traits>
@@ -93,7 +94,8 @@ struct RowSums {
 // ---- a worker's piece of a row --------------------------------------------------------
 
 // A worker's waves share a row: chunk lane + 64 (wave + waves k) of eight elements, k < C. One wave takes rows of up to
-// 512 elements, four such workers in a workgroup; longer rows have a workgroup of up to eight waves.
+// 512 elements, four such workers in a workgroup; longer rows have a workgroup of up to sixteen waves forward and eight
+// backward.
 template <bool ONE>
 constexpr int most_threads() { return ONE ? 256 : 64 * kMostWaves; }
 constexpr int kBackwardThreads = 512;
@@ -786,7 +788,8 @@ int backward_chunks(int64_t dim) { return dim <= 4096 ? 1 : dim <= 8192 ? 2 : di
 // kBackwardRows, since each worker's sums are written once and read once
 int backward_run(int64_t rows, int64_t dim) {
   const int w = waves_of(dim, backward_chunks(dim));
-  const int64_t workers = 256 * (int64_t)(kBackwardWaves / w > 0 ? kBackwardWaves / w : 1), n = (rows + workers - 1) / workers;
+  const int64_t workers = 256 * (int64_t)(kBackwardWaves / w > 0 ? kBackwardWaves / w : 1);
+  const int64_t n = (rows + workers - 1) / workers;
   return (int)(n < kBackwardRows ? kBackwardRows : n);
 }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -810,7 +813,8 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
     return hipSuccess;
   }
   const int run = backward_run(a.n.rows, a.n.dim), workers = (a.n.rows + run - 1) / run, groups = a.n.groups.groups;
-  const int need = (a.dscale || a.dweight ? kSumScale : 0) | (a.dshift || a.dbias || (a.dscale && a.n.bias) ? kSumShift : 0) |
+  const int need = (a.dscale || a.dweight ? kSumScale : 0) |
+                   (a.dshift || a.dbias || (a.dscale && a.n.bias) ? kSumShift : 0) |
                    (a.dgate || a.dpost_weight ? kSumGate : 0);
   float* parts = static_cast<float*>(workspace);
   hipError_t e = with_groups(a.n, [&](auto grouped) {
@@ -822,9 +826,11 @@ hipError_t backward(const NormBackward& a, void* workspace, hipStream_t s) {
       constexpr bool ONE = decltype(o)::value;
       constexpr int C = decltype(c)::value;
       if (a.branch.p && a.n.post != BSQ_NORM_NONE)
-        hipLaunchKernelGGL((block_norm_backward<E, ONE, C, G, true>), dim3(blocks), dim3(threads), 0, s, a, run, need, parts);
+        hipLaunchKernelGGL((block_norm_backward<E, ONE, C, G, true>), dim3(blocks), dim3(threads), 0, s, a, run, need,
+                           parts);
       else
-        hipLaunchKernelGGL((block_norm_backward<E, ONE, C, G, false>), dim3(blocks), dim3(threads), 0, s, a, run, need, parts);
+        hipLaunchKernelGGL((block_norm_backward<E, ONE, C, G, false>), dim3(blocks), dim3(threads), 0, s, a, run, need,
+                           parts);
       return hipGetLastError();
     };
     if (one) return go(std::true_type{}, chunks_t<1>{});

@@ -78,7 +78,8 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, uint4 v, int n, int N) 
 template <int BM, int BN, int TROW>
 __device__ __forceinline__ void load_tile_rows(uint8_t* tile, const uint16_t* r, int64_t ldr, int M, int N, int m0,
                                                int n0, int tid) {
-  constexpr int CPR = BN / 8, IT = BM * CPR / kThreads, U = IT % 16 == 0 ? 16 : IT % 12 == 0 ? 12 : IT % 8 == 0 ? 8 : IT;
+  constexpr int CPR = BN / 8, IT = BM * CPR / kThreads;
+  constexpr int U = IT % 16 == 0 ? 16 : IT % 12 == 0 ? 12 : IT % 8 == 0 ? 8 : IT;
   static_assert(BM * CPR % kThreads == 0 && IT % U == 0, "whole steps");
 #pragma unroll
   for (int i0 = 0; i0 < IT; i0 += U) {
@@ -108,7 +109,8 @@ __device__ __forceinline__ void put_tile_rows(const uint8_t* tile, uint16_t* y, 
   for (int idx = tid; idx < BM * CPR; idx += kThreads) {
     const int ml = idx / CPR, c = idx - ml * CPR, n = n0 + 8 * c;
     if (m0 + ml >= M) break;  // rows only grow with idx
-    if (n < N) store_chunk(y + (int64_t)(m0 + ml) * ldy + n, *reinterpret_cast<const uint4*>(tile + ml * TROW + c * 16), n, N);
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + ml * TROW + c * 16);
+    if (n < N) store_chunk(y + (int64_t)(m0 + ml) * ldy + n, v, n, N);
   }
 }
 

@@ -2,8 +2,8 @@
 //
 // Bound by memory: every element is read and written once; an angle costs some 55 instructions
 // and serves all heads of its token, so a workgroup first puts the cosines and sines of its tokens
-// into LDS and then streams the tokens' heads, 16 bytes of each half of eight pairs (four of fp32) a thread and step. 8192 tokens of
-// 40 heads of 128, fp16: 168 MB in 32.8 us, 5.1 TB/s, what a copy reaches; 48 tokens of 40 heads 3.1 us, a launch.
+// into LDS and then streams the tokens' heads, 16 bytes of each half of eight pairs (four of fp32) a thread and step.
+// 8192 tokens of 40 heads of 128, fp16: 168 MB in 32.8 us, 5.1 TB/s, what a copy reaches; 48 tokens of 40 heads 3.1 us, a launch.
 //
 // With several axes (bsq_rope_axes) the angles take their pair's axis' position, and nothing else changes: 14400 tokens
 // of 48 heads of 128, bf16, three axes: 354 MB in 65 us, 5.4 TB/s.
