@@ -1,5 +1,8 @@
 // fp8r W8A8 GEMM with an epilogue (include/bsq_block.h): the tiles of gemm_fp8_tile.hpp, whose sums go through bias,
 // activation, gate and residual (epilogue.hpp) before they are rounded.
+//
+// Bound by the matrix cores' feed, as without an epilogue: 4096 x 10240 x 2560 with gelu_tanh 128 us, 1.7 PFLOP/s (the plain
+// linear 127). Forced onto other tiles: 256 x 256 145 us, 256 x 192 155, 128 x 128 alone with four buffers 191.
 #include "epilogue.hpp"
 #include "gemm_fp8_tile.hpp"
 

@@ -16,13 +16,16 @@ if torch.cuda.is_available():
 ACTS = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu": 3}
 
 
-def operands(fmt, M, N, K, seed):
-    """(the entry point, the plain linear, its operands on the GPU, the fp64 product, a bound of its error before rounding)
-
-    Products are exact and are summed in fp32 (K 2^-24 of their magnitudes), but the e4m3 matrix instruction first aligns
+def product_bound(fmt, K, magnitudes):
+    """Products are exact and are summed in fp32 (K 2^-24 of their magnitudes), but the e4m3 matrix instruction first aligns
     eight products at a time to the largest, to 13 bits below its leading one, cutting off what is below: one product of
     2^16 beside 1.875 x 2^3 leaves 8, beside 1.875 x 2^2 nothing, and of 62 ones beside two of +-2^16 the six in the same
     eight are lost. Seven of eight lose less than 2^-13 of the eighth each, at most 7 x 2^-13 of the sum of magnitudes."""
+    return (K * 2.0 ** -24 + (7 * 2.0 ** -13 if fmt == "fp8r" else 0.0)) * magnitudes
+
+
+def operands(fmt, M, N, K, seed):
+    """(the entry point, the plain linear, its operands on the GPU, the fp64 product, a bound of its error before rounding)"""
     g = torch.Generator().manual_seed(seed)
     if fmt == "fp8r":
         c = lambda *s: (torch.randn(*s, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
@@ -44,8 +47,7 @@ def operands(fmt, M, N, K, seed):
         args = [t.cuda() for t in (xq, xs, gx, w, ws, gw)]
     f = L.bsq_gemm_fp8r_q_epilogue if fmt == "fp8r" else L.bsq_gemm_nvfp4_q_epilogue
     plain = L.bsq_gemm_fp8r_q if fmt == "fp8r" else L.bsq_gemm_nvfp4_q
-    bound = (K * 2.0 ** -24 + (7 * 2.0 ** -13 if fmt == "fp8r" else 0.0)) * (np.abs(x64) @ np.abs(w64).T)
-    return f, plain, args, x64 @ w64.T, bound
+    return f, plain, args, x64 @ w64.T, product_bound(fmt, K, np.abs(x64) @ np.abs(w64).T)
 
 
 def bf(g, *s, size=1.0):

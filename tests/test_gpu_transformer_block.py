@@ -9,7 +9,7 @@ import torch
 from oracle import block
 from oracle.codec import e2m1_decode, e4m3_decode
 from tests.block_util import f64, forward_bounds, rounded
-from tests.test_gpu_epilogue import check
+from tests.test_gpu_epilogue import check, product_bound
 from tests.test_gpu_rope_axes import bound
 
 pytestmark = pytest.mark.gpu
@@ -93,7 +93,7 @@ def test_block(fmt):
 
     def product(layer, codes):
         a = layer.decoded(codes)
-        return a @ layer.value.T, np.abs(a) @ np.abs(layer.value).T
+        return a @ layer.value.T, product_bound(fmt, a.shape[1], np.abs(a) @ np.abs(layer.value).T)
 
     def check_codes(layer, codes, x, scale, shift):
         _, _, y, ey = forward_bounds(f64(x), "layer", EPS, group, scale=f64(scale), shift=f64(shift))
@@ -112,7 +112,7 @@ def test_block(fmt):
     if fmt == "fp8r":
         codes[1][~torch.from_numpy(live)] = 0
     h = qkv(codes)
-    check(h, *product(qkv, codes), D, qkv.bias, "none", None, None, None)
+    check(h, *product(qkv, codes), qkv.bias, "none", None, None, None)
     heads = h.view(T, 3 * HEADS, DIM)
     q0 = heads[:, :2 * HEADS].cpu()
     L.bsq_rope_axes(heads[:, :2 * HEADS], pos.cuda(), inv.cuda(), [DIM // 4, DIM // 4], y=heads[:, :2 * HEADS])
@@ -125,7 +125,7 @@ def test_block(fmt):
     codes = out.encode(a)
     before = x.clone()
     assert out(codes, gate=gate1, residual=x, starts=st, y=x) is x   # the stream, in place
-    check(x, *product(out, codes), D, out.bias, "none", gate1, before, group)
+    check(x, *product(out, codes), out.bias, "none", gate1, before, group)
     # the same by the norm's own gated residual: the branch rounded on its way
     branch = out(codes)
     (codes2, _), (codes3, other) = up.norm(x, scale=scale2, shift=shift2, starts=st), up.norm(
@@ -139,11 +139,11 @@ def test_block(fmt):
     if fmt == "fp8r":
         codes2[1][~torch.from_numpy(live)] = 0
     m = up(codes2, act=L.BSQ_ACT_GELU_TANH)
-    check(m, *product(up, codes2), D, up.bias, "gelu_tanh", None, None, None)
+    check(m, *product(up, codes2), up.bias, "gelu_tanh", None, None, None)
     codes = down.encode(m)
     before = x.clone()
     down(codes, gate=gate2, residual=x, starts=st, y=x)
-    check(x, *product(down, codes), INNER, down.bias, "none", gate2, before, group)
+    check(x, *product(down, codes), down.bias, "none", gate2, before, group)
     assert torch.equal(x[starts[-1]:], start[starts[-1]:])
 
 
