@@ -123,6 +123,8 @@ def test_forward_encoded(T, D, norm, post, groups, starts, want, kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("T,D,norm,post,groups,starts,want", CASES + [
+    (420, 1536, "rms", "layer", 6, None, ALL),
+    (700, 4096, "layer", None, 3, [0, 200, 201, 690], dict(branch=1, gate=1, scale=1, shift=1)),
     (9, 64, None, "rms", 2, [0, 4, 8], dict(branch=1, gate=1, post_weight=1)),
     (40, 2560, None, None, 2, None, dict(branch=1, gate=1)),
     (5000, 64, "rms", "rms", 2, [0, 4999, 5000], ALL), (2000, 4096, "layer", None, 1, None, dict(weight=1, bias=1)),
