@@ -940,6 +940,10 @@ def bsq_block_norm_workspace_bytes(rows, dim, groups=1):
     return lib.bsq_block_norm_workspace_bytes(rows, dim, groups)
 
 
+_GRADIENTS = ("scale", "shift", "gate", "weight", "bias", "post_weight")
+_NO_GRADIENTS = [None] * len(_GRADIENTS)
+
+
 def bsq_block_norm_backward(dy, dx_out, x_out, norm=BSQ_NORM_RMS, eps=1e-6, weight=None, bias=None, scale=None,
                             shift=None, branch=None, gate=None, post=BSQ_NORM_NONE, post_weight=None, starts=None,
                             post_eps=None, need=None, dx=None, dbranch=None, workspace=None):
@@ -964,26 +968,27 @@ def bsq_block_norm_backward(dy, dx_out, x_out, norm=BSQ_NORM_RMS, eps=1e-6, weig
     if branch is not None:
         bp, bs = _row_stride(branch, shape, dtype, dev, "branch")
     if dx is None and (need is None or "x" in need or (of_branch and not own)):
-        dx = torch.empty(shape, dtype=dtype, device=dev)
+        dx = torch.empty_like(like, memory_format=torch.contiguous_format)
     if dbranch is None and own:
-        dbranch = torch.empty(shape, dtype=dtype, device=dev)
+        dbranch = torch.empty_like(like, memory_format=torch.contiguous_format)
     if dx is not None:
         xp, xs = _row_stride(dx, shape, dtype, dev, "dx")
     if dbranch is not None:
         hp, hs = _row_stride(dbranch, shape, dtype, dev, "dbranch")
-    out = {"x": dx, "branch": dbranch if dbranch is not None or not of_branch else dx}
+    out = dict.fromkeys(("x", "branch") + _GRADIENTS)
+    out["x"], out["branch"] = dx, dbranch if dbranch is not None or not of_branch else dx
     # the vectors' gradients: those of the groups in one tensor, those that all share in another
-    vectors = []
-    for names, size in (((("scale", scale), ("shift", shift), ("gate", gate)), (groups, D)),
-                        ((("weight", weight), ("bias", bias), ("post_weight", post_weight)), (D,))):
+    for size, names in (((groups, D), (("scale", scale), ("shift", shift), ("gate", gate))),
+                        ((D,), (("weight", weight), ("bias", bias), ("post_weight", post_weight)))):
         asked = [name for name, v in names if v is not None and (need is None or name in need)]
-        grads = iter(torch.empty((len(asked), *size), dtype=torch.float32, device=dev).unbind(0) if asked else ())
-        for name, _ in names:
-            out[name] = t = next(grads) if name in asked else None
-            vectors.append(None if t is None else t.data_ptr())
+        if len(asked) == 1:
+            out[asked[0]] = torch.empty(size, dtype=torch.float32, device=dev)
+        elif asked:
+            out.update(zip(asked, torch.empty((len(asked), *size), dtype=torch.float32, device=dev).unbind(0)))
+    vectors = [None if out[k] is None else out[k].data_ptr() for k in _GRADIENTS]
     n = 0
     if workspace is None:
-        if T and any(v is not None for v in vectors):
+        if T and vectors != _NO_GRADIENTS:
             n = lib.bsq_block_norm_workspace_bytes(T, D, groups)
             workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
     elif workspace.device != dev:

@@ -246,3 +246,26 @@ def test_few_rows_and_many_columns(fmt, M, N):
     g = torch.Generator().manual_seed(M)
     bias, residual, gate = bf(g, N), bf(g, M, N), bf(g, 1, N)
     check(f(*args, bias=bias, act=ACTS["gelu"], residual=residual, gate=gate), v, bound, bias, "gelu", gate, residual, None)
+
+
+@pytest.mark.parametrize("fmt,K", [("fp8r", 96), ("nvfp4", 96), ("nvfp4", 256)])
+def test_offsets_past_32_bits(fmt, K):
+    """Outputs and residuals of more than 2^31 elements: the last rows are those of a call of their own."""
+    M, N, last = 70_001, 32_768, 264
+    g = torch.Generator(device="cuda").manual_seed(K)
+    code = lambda *s: torch.randint(0, 120, s, dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    if fmt == "fp8r":
+        f = L.bsq_gemm_fp8r_q_epilogue
+        x, w = (code(M, K), torch.rand(M, device="cuda", generator=g)), (code(N, K), torch.rand(N, device="cuda", generator=g))
+        call = lambda rows, **kw: f(x[0][rows], x[1][rows], *w, **kw)  # noqa: E731
+    else:
+        f, one = L.bsq_gemm_nvfp4_q_epilogue, torch.ones(1, device="cuda")
+        x, w = (code(M, K // 2), code(M, K // 16)), (code(N, K // 2), code(N, K // 16), one)
+        call = lambda rows, **kw: f(x[0][rows], x[1][rows].clone(), one, *w, **kw)  # noqa: E731  (4-byte aligned scales)
+    residual = torch.randint(-3, 4, (M, N), dtype=torch.int8, device="cuda", generator=g).bfloat16()
+    bias = torch.randn(N, device="cuda", generator=g).bfloat16()
+    y = call(slice(None), bias=bias, act=ACTS["silu"], residual=residual)
+    tail = slice(M - last, M)
+    assert torch.equal(y[tail], call(tail, bias=bias, act=ACTS["silu"], residual=residual[tail]))
+    call(slice(None), bias=bias, act=ACTS["silu"], residual=residual, y=residual)
+    assert torch.equal(y, residual)
