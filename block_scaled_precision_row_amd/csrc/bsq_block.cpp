@@ -65,7 +65,8 @@ bsq::NormArgs norm_args(const bsq_block* b) {
 }
 bsq::Rows rows_of(const void* p, int64_t stride) { return bsq::Rows{const_cast<void*>(p), stride}; }
 
-// the threads of a launch (block_norm.hip has one workgroup a row, or four rows of up to 512) stay below 2^31
+// the threads of a forward launch (block_norm.hip has one workgroup a row, or four rows of up to 512) stay below 2^31;
+// the gradient has at most 3072 workers, whatever the rows
 bool launch_fits(int64_t rows, int64_t dim) {
   const int64_t waves = dim <= 2048 ? (dim + 511) / 512 : (dim + 1023) / 1024;
   return rows * waves * 64 < ((int64_t)1 << 31) - 256;
@@ -172,7 +173,6 @@ bsq_status bsq_block_norm_backward(const bsq_block* b, const void* dy, int64_t d
   if (b->rows > 1 && ((dx && dx == dy && dx_stride != dy_stride) || (dx && dx == dx_out && dx_stride != dx_out_stride) ||
                       (dbranch && dbranch == branch && dbranch_stride != branch_stride)))
     return BSQ_ERR_SHAPE;
-  if (!launch_fits(b->rows, b->dim)) return BSQ_ERR_SHAPE;
   const bool vectors = dscale || dshift || dgate || dweight || dbias || dpost_weight;
   if (b->rows == 0 && !vectors) return BSQ_OK;
   if (b->rows > 0) {
