@@ -66,7 +66,7 @@ bsq::NormArgs norm_args(const bsq_block* b) {
 bsq::Rows rows_of(const void* p, int64_t stride) { return bsq::Rows{const_cast<void*>(p), stride}; }
 
 // the threads of a forward launch (block_norm.hip has one workgroup a row, or four rows of up to 512) stay below 2^31;
-// the gradient has at most 3072 workers, whatever the rows
+// the gradient has at most twelve workers a compute unit, whatever the rows
 bool launch_fits(int64_t rows, int64_t dim) {
   const int64_t waves = dim <= 2048 ? (dim + 511) / 512 : (dim + 1023) / 1024;
   return rows * waves * 64 < ((int64_t)1 << 31) - 256;

@@ -78,7 +78,9 @@ bsq_status bsq_rope_axes(bsq_dtype dtype, const void* x, int64_t x_stride_t, int
  *     their strides apart (>= dim where groups > 1; multiples of 8)
  * 8 <= dim <= 16384, dim % 8 == 0, 0 <= rows <= 2^30; strides of rows in elements,
  * multiples of 8, >= dim and < 2^40 (x and branch: also 0, one row for all; rows == 1: any multiple of 8);
- * pointers 16-byte aligned.
+ * pointers 16-byte aligned. bsq_block_norm has a workgroup for each row or four of them: rows times the waves of a row,
+ * ceil(dim / 512) up to dim 2048 and ceil(dim / 1024) above, stay below 2^25 - 4 there (BSQ_ERR_SHAPE otherwise; longer
+ * tensors are several calls, since rows are independent). bsq_block_norm_backward takes all 2^30.
  * eps, post_eps >= 0 and finite. post_weight needs a post norm. (BSQ_ERR_ARG for an unknown dtype, norm or format,
  * eps out of range, vectors of a norm that is not there.)
  */

@@ -46,3 +46,13 @@ def test_gradient_of_more_rows_than_a_launch_has_workgroups():
         e = min(a + (1 << 22), T - 9)
         part = L.bsq_block_norm_backward(dy[a:e], None, x[a:e], norm=L.BSQ_NORM_RMS, eps=0.0, weight=w, bias=b, need=("x",))
         assert torch.equal(dx[a:e], part["x"]), a
+
+
+def test_most_rows_of_a_forward_launch():
+    T = (1 << 25) - 5
+    x = rows_of_signs(T, 2)[0]
+    w = torch.linspace(-2, 2, D, device="cuda").bfloat16()
+    y = L.bsq_block_norm(x, norm=L.BSQ_NORM_RMS, eps=0.0, weight=w)[0]
+    assert torch.equal(y, x * w)
+    with pytest.raises(L.BsqError):
+        L.bsq_block_norm(x[:1].expand(T + 1, D), norm=L.BSQ_NORM_RMS, weight=w)
