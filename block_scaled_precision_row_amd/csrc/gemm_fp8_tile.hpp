@@ -138,6 +138,11 @@ __device__ __forceinline__ void lora_update_lds(v16f (&acc)[TN][TM], const uint8
 template <int NS>
 constexpr bool hand_ordered() { return NS == 2; }
 
+// the output of a tile: memory that nothing else in the call points to, but where an epilogue may have it as its residual
+template <class Finish>
+using OutputOf =
+    typename std::conditional<std::is_same<Finish, NoFinish>::value, uint16_t* __restrict__, uint16_t*>::type;
+
 // OQ: quantized output for the next linear -- 0 none, 1 nvfp4 blocks in the epilogue, 2 the
 // row maxima of the fp8r encoding (YQuant). HS: the hand-ordered K loop (K % 128 == 0). LL:
 // where the adapter's T and B rows are read (LoraLds). WPE: waves per SIMD the registers are
@@ -147,7 +152,7 @@ constexpr bool hand_ordered() { return NS == 2; }
 template <int BM, int BN, int NS, bool LORA, int OQ, bool HS, int LL, class Finish = NoFinish>
 __device__ __forceinline__ void fp8_tile(const uint8_t* __restrict__ xq, const float* __restrict__ sx,
                                          const uint8_t* __restrict__ w, const float* __restrict__ sw,
-                                         uint16_t* __restrict__ y, int64_t ldy, int M, int N, int K,
+                                         OutputOf<Finish> y, int64_t ldy, int M, int N, int K,
                                          const uint16_t* lt, const uint16_t* lb, int rank, int stream_y,
                                          const YQuant& q, int bid, const Finish& finish = Finish{}) {
   constexpr bool kFinish = !std::is_same<Finish, NoFinish>::value;
