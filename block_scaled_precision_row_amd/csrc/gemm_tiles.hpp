@@ -139,6 +139,25 @@ struct W4Cfg {
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
+// The block scales of one row of a W4A4 stage where K % 256 != 0 (rows of scales are then not 16-byte aligned, which an LDS
+// DMA asks for): a thread takes them through registers. Row r of the stage is W row n0 + r, and from BN on Xq row
+// m0 + r - BN. `left` of its scales (an even number, 0 past K or past the matrix), 16 at most, are read `from` bytes into that
+// operand's scales, and 16 bytes, the rest of them 0, go to `lds` of the stage, where the DMA would have put them (-1: no row).
+struct ScaleRowLoad {
+  bool w;
+  int64_t from;
+  int left, lds;
+};
+template <int BM, int BN>
+__host__ __device__ constexpr ScaleRowLoad scale_row_load(int r, int kt, int m0, int n0, int M, int N, int K) {
+  using C = W4Cfg<BM, BN>;
+  const bool w = r < BN;
+  const int row = w ? n0 + r : m0 + r - BN, ks = K >> 4, at = kt * (C::KSTAGE / 16), left = ks - at;
+  const bool there = left > 0 && r < BM + BN && row < (w ? N : M);
+  return ScaleRowLoad{w, (int64_t)row * ks + at, there ? left : 0,
+                      r < BM + BN ? (w ? C::SA_OFF + 16 * r : C::SB_OFF + 16 * (r - BN)) : -1};
+}
+
 // weight-only W4A16 / W8A16 (gemm_a16.hip): 128-deep stages of bf16 X rows (256 bytes), packed
 // E2M1 (64 bytes) or E4M3 (128 bytes) W rows, and for nvfp4 8 block-scale bytes per W row.
 template <int BM, int BN, bool FP4>

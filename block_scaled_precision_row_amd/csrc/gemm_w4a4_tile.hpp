@@ -66,9 +66,9 @@ __device__ __forceinline__ uint32_t dword_of(const uint4& q) {
   return T == 0 ? q.x : T == 1 ? q.y : T == 2 ? q.z : q.w;
 }
 
-// The block scales of a stage, for any K (K % 256 != 0: rows of scales are then not 16-byte aligned, which an LDS DMA
-// asks for): 16 bytes of each W and Xq row into registers, at any address, and from there to where the DMA would have put
-// them. Scales past K and rows past the matrix are 0 (the codes there are read as 0; a scale's NaN must not meet them).
+// The block scales of a stage, for any K (scale_row_load of gemm_tiles.hpp): 16 bytes of each W and Xq row into registers, at
+// any even address, and from there to LDS. Scales past K and rows past the matrix are 0 (the codes there are read as 0; a
+// scale's NaN must not meet them).
 template <int BM, int BN>
 struct ScaleRows {
   static constexpr int N = (BM + BN + kThreads - 1) / kThreads;
@@ -77,33 +77,29 @@ struct ScaleRows {
   };
   uint4 v[N];
   __device__ __forceinline__ void load(const DecArgs& a, int m0, int n0, int kt, int tid) {
-    const int M = (int)a.M, K = (int)a.K, ks = K >> 4, at = kt * (kStageK / 16), left = ks - at;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int r = tid + j * kThreads;
-      const bool w = r < BN;
-      const int row = w ? n0 + r : m0 + r - BN;
+      const ScaleRowLoad l = scale_row_load<BM, BN>(tid + j * kThreads, kt, m0, n0, (int)a.M, (int)a.N, (int)a.K);
       v[j] = make_uint4(0, 0, 0, 0);
-      if (left <= 0 || r >= BM + BN || row >= (w ? (int)a.N : M)) continue;
-      const uint8_t* p = (w ? a.ws : a.xs) + (int64_t)row * ks + at;
-      if (left >= 16) {
+      if (l.left == 0) continue;
+      const uint8_t* p = (l.w ? a.ws : a.xs) + l.from;
+      if (l.left >= 16) {
         const Any x = *reinterpret_cast<const Any*>(p);
         v[j] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
       } else {  // (an even number of them: K % 32 == 0)
         uint32_t x[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (2 * e < left) x[e >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+          if (2 * e < l.left) x[e >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
         v[j] = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
   }
   __device__ __forceinline__ void store(uint8_t* stage, int tid) const {
-    using C = W4Cfg<BM, BN>;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int r = tid + j * kThreads;
-      if (r < BM + BN) *reinterpret_cast<uint4*>(stage + (r < BN ? C::SA_OFF + 16 * r : C::SB_OFF + 16 * (r - BN))) = v[j];
+      const int at = scale_row_load<BM, BN>(tid + j * kThreads, 0, 0, 0, 0, 0, 0).lds;
+      if (at >= 0) *reinterpret_cast<uint4*>(stage + at) = v[j];
     }
   }
 };
