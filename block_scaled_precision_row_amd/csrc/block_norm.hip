@@ -234,7 +234,6 @@ __device__ __forceinline__ float larger(float a, float b) { return __builtin_ele
 // One row a worker: with some 20 waves on a compute unit the loads of other rows run under a row's sums.
 template <class E, bool ONE, int C, bool GROUPED>
 __global__ __launch_bounds__(most_threads<ONE>()) void block_norm(NormForward a) {
-  typedef typename E::elem elem;
   __shared__ Slots slots;
   const NormArgs& n = a.n;
   const Place<ONE, C> me(n.dim);
