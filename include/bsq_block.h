@@ -142,7 +142,9 @@ bsq_status bsq_block_norm_backward(const bsq_block* block, const void* dy, int64
  * The pre-quantized linears of bsq.h (bsq_gemm_fp8r_q, bsq_gemm_nvfp4_q: operands, routes and errors as there)
  * with an epilogue:
  *   y[m][n] = bf16( residual[m][n] + gate[g(m)][n] * act( (x w^T)[m][n] + bias[n] ) )
- * where (x w^T) is their fp32 result before its rounding and every step is fp32, rounded once at the end.
+ * where (x w^T) is their result before its rounding and every step after it is fp32, rounded once at the end. Products are
+ * summed in fp32; for fp8r the e4m3 matrix instruction takes them eight at a time and first cuts each one off below 2^-13
+ * of the largest of the eight (bsq.h; nvfp4's f16 instruction cuts nothing off).
  *   BSQ_ACT_NONE       v
  *   BSQ_ACT_SILU       v / (1 + exp(-v))
  *   BSQ_ACT_GELU_TANH  v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
