@@ -149,6 +149,7 @@ bsq_status bsq_block_norm_backward(const bsq_block* block, const void* dy, int64
  *   BSQ_ACT_SILU       v / (1 + exp(-v))
  *   BSQ_ACT_GELU_TANH  v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
  *   BSQ_ACT_GELU       v Phi(v), Phi the normal distribution: to 2^-15 of itself for v >= -5, below that to 4e-7
+ * (silu and gelu_tanh to 2^-15 of themselves, by the hardware's exp2 and reciprocal; what would be below 2^-119 may be 0.)
  *   bias     [N] bf16 or NULL (0)
  *   gate     [groups] rows of N bf16, gate_stride apart (>= N where groups > 1), 2-byte aligned, or NULL (1)
  *   residual [M][residual_stride] bf16 (residual_stride >= N), 16-byte aligned, or NULL (0); y may be residual with
