@@ -72,7 +72,8 @@ bsq_status bsq_rope_axes(bsq_dtype dtype, const void* x, int64_t x_stride_t, int
  * Vectors that are NULL are left out (weight, gate, post_weight count as 1, scale, shift, bias as 0).
  * norm == BSQ_NORM_NONE: there is no y (no weight, bias, scale, shift), x_out alone.
  * Rows are held in fp32 from their load to their store: y is formed from x_out as it is before its
- * rounding, statistics are sums in fp32 (they overflow where |x| reaches 2^57).
+ * rounding, statistics are sums of squares in fp32: they overflow where |x| reaches 2^57, and with eps 0 they lose what is
+ * below 2^-56 (a row whose largest |x|, or |x - mean|, is less; one of zeros is 0 / 0, NaN).
  *   dtype     of all tensors (any of the three)
  *   weight, bias, post_weight [dim]; scale, shift, gate [groups] rows of dim,
  *     their strides apart (>= dim where groups > 1; multiples of 8)
