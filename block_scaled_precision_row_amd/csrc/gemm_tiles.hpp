@@ -1,8 +1,8 @@
 // Tile configurations of the LDS-DMA GEMMs and the address arithmetic of every LDS-DMA load,
 // as host- and device-callable integer functions. The kernels issue their loads through
-// these functions, and a host program (tests/dma_audit.hip) enumerates every load of every
-// launched configuration through the same functions and checks its LDS destination and its
-// buffer offsets.
+// these functions, and host programs (tests/dma_audit.hip, and tests/block_dma_audit.hip for the
+// linears with an epilogue) enumerate every load of every launched configuration through the same
+// functions and check its LDS destination and its buffer offsets.
 //
 // An LDS-DMA load (buffer_load_dword[x4] ... lds) makes lane l fetch 4 or 16 bytes at
 // rsrc.base + voffset(l) + soffset (the buffer's range check covers both offsets: reads at or
